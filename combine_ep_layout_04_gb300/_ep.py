@@ -1,4 +1,4 @@
-"""ctypes binding of libep.so: the C ABI of include/ep.h, same names, argument
+"""ctypes binding of libep.so: the C ABI of include/ep.h and ep_ops.h, same names, argument
 marshalling only.  Every step of the layer runs in the library's CUDA kernels;
 there is no other code path.  If libep.so is missing, importing this module
 raises."""
@@ -18,6 +18,8 @@ EP_ERR_CUDA = 4
 EP_ERR_NOT_READY = 5
 EP_DEBUG_DISABLE_CONSUMER = 0x1
 EP_DEBUG_DEVICE_COUNTERS = 0x2
+EP_DTYPE_F32 = 0
+EP_DTYPE_BF16 = 1
 
 _STATUS_NAMES = {0: "EP_OK", 1: "EP_ERR_INVALID_ARG", 2: "EP_ERR_CAPACITY", 3: "EP_ERR_TIMEOUT",
                  4: "EP_ERR_CUDA", 5: "EP_ERR_NOT_READY"}
@@ -78,6 +80,7 @@ lib = ctypes.CDLL(LIB_PATH)
 
 _h = ctypes.c_void_p
 _p = ctypes.c_void_p
+_i32, _i64, _f32 = ctypes.c_int32, ctypes.c_int64, ctypes.c_float
 _sigs = {
     "ep_config_init": ([ctypes.POINTER(ep_config)] + [ctypes.c_int32] * 5, ctypes.c_int),
     "ep_config_check": ([ctypes.POINTER(ep_config)], ctypes.c_int),
@@ -110,6 +113,21 @@ _sigs = {
                          ctypes.POINTER(ctypes.c_int32)], ctypes.c_int),
     "ep_sm_split_destroy": ([_h], ctypes.c_int),
     "ep_sm_ids": ([_p, ctypes.c_int32, _p], ctypes.c_int),
+    # include/ep_ops.h
+    "ep_rms_norm": ([_i64, _i32, _p, _i64, _p, _i64, _p, _i32, _f32, _p, _i64, _p, _i64, _p, _i64, _p, _i64, _p, _p],
+                    ctypes.c_int),
+    "ep_rms_norm_backward_workspace": ([_i64, _i32], _i64),
+    "ep_rms_norm_backward": ([_i64, _i32, _p, _i64, _p, _i64, _p, _i32, _p, _p, _i64, _p, _i64, _p, _p, _i64, _p],
+                             ctypes.c_int),
+    "ep_route_workspace": ([_i64, _i32], _i64),
+    "ep_route": ([_i64, _i32, _i32, _p, _i32, _i64, _p, _i32, _p, _p, _i32, _p, _f32, _p, _p, _p, _p, _p, _i64, _p],
+                 ctypes.c_int),
+    "ep_route_backward": ([_i64, _i32, _i32, _p, _i32, _i64, _i32, _p, _p, _p, _p, _p, _p, _p, _i64, _p],
+                          ctypes.c_int),
+    "ep_expert_product": ([_i64, _i64, _i32, _i32, _i32, _i32, _p, _i64, _p, _i64, _p, _p, _p, _p, _p, _p, _i64, _p,
+                           _i64, _p, _i64, _p, _p], ctypes.c_int),
+    "ep_pick_sum": ([_i64, _i64, _i32, _i32, _i32, _i32, _p, _i64, _p, _p, _p, _p, _p, _p, _p, _i64, _p, _p],
+                    ctypes.c_int),
 }
 for _name, (_args, _res) in _sigs.items():
     _f = getattr(lib, _name)
@@ -273,3 +291,38 @@ def ep_sm_split_destroy(s) -> None:
 
 def ep_sm_ids(stream: int, blocks: int, out_ptr: int) -> None:
     check(lib.ep_sm_ids(stream, blocks, out_ptr), "ep_sm_ids")
+
+
+# ------------------------------------------------ operators (include/ep_ops.h)
+# Arguments in the header's order; pointers and streams are whole numbers, None is NULL.
+
+def ep_rms_norm(*args) -> None:
+    check(lib.ep_rms_norm(*args), "ep_rms_norm")
+
+
+def ep_rms_norm_backward_workspace(tokens: int, hidden: int) -> int:
+    return lib.ep_rms_norm_backward_workspace(tokens, hidden)
+
+
+def ep_rms_norm_backward(*args) -> None:
+    check(lib.ep_rms_norm_backward(*args), "ep_rms_norm_backward")
+
+
+def ep_route_workspace(tokens: int, experts: int) -> int:
+    return lib.ep_route_workspace(tokens, experts)
+
+
+def ep_route(*args) -> None:
+    check(lib.ep_route(*args), "ep_route")
+
+
+def ep_route_backward(*args) -> None:
+    check(lib.ep_route_backward(*args), "ep_route_backward")
+
+
+def ep_expert_product(*args) -> None:
+    check(lib.ep_expert_product(*args), "ep_expert_product")
+
+
+def ep_pick_sum(*args) -> None:
+    check(lib.ep_pick_sum(*args), "ep_pick_sum")

@@ -1,0 +1,340 @@
+// ep_norm.cu -- residual addition and root-mean-square norm with an output in
+// bf16 or in 8-bit rows, and its gradient (include/ep_ops.h).
+//
+// Both directions are bound by memory: forward reads x and residual and writes
+// h and y once (7 bytes a value with an 8-bit y), backward reads three rows
+// and writes one (8 bytes a value).  A row stays in registers between the pass
+// that sums it and the pass that uses the sum, so nothing is read twice: a
+// team of warps holds a row, eight neighbouring values (16 bytes) to a lane in
+// each of VPT steps.  Rows up to 1024 columns take one warp, eight rows to a
+// block and no barrier; longer rows take a block of ceil(columns / 1024) warps.
+#include "ep_ops.cuh"
+
+namespace {
+
+using namespace ep;
+
+constexpr int kMaxHidden = 32768;
+constexpr int kTeams = 8;      // rows per block where a row takes one warp
+
+struct NormParams {
+    int64_t tokens;
+    const __nv_bfloat16 *x, *residual;
+    const void *weight;
+    __nv_bfloat16 *out, *residual_out;
+    uint8_t *values;
+    float *scales, *rstd;
+    int64_t x_stride, residual_stride, out_stride, value_stride, scale_stride, residual_out_stride;
+    int hidden, weight_dtype;
+    float eps;
+};
+
+// Sum over a team: one warp, or the whole block.  Every lane gets the sum, in
+// an order that does not depend on timing.
+template <bool kWide>
+__device__ __forceinline__ float team_sum(float v, float *smem) {
+    v = warp_sum(v);
+    if (!kWide) return v;
+    const int warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    if ((threadIdx.x & 31) == 0) smem[warp] = v;
+    __syncthreads();
+    return warp_sum((threadIdx.x & 31) < warps ? smem[threadIdx.x & 31] : 0.0f);
+}
+
+template <int VPT, bool kWide>
+__global__ void __launch_bounds__(kWide ? 1024 : 32 * kTeams) norm_kernel(NormParams p) {
+    __shared__ float part[32];
+    const int64_t t = kWide ? blockIdx.x : static_cast<int64_t>(blockIdx.x) * kTeams + (threadIdx.x >> 5);
+    if (t >= p.tokens) return;
+    const int lane = kWide ? threadIdx.x : threadIdx.x & 31;
+    const int width = kWide ? blockDim.x : 32;
+    const int nvec = p.hidden >> 3;
+    float h[VPT][8];
+    float sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+        const int v = i * width + lane;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) h[i][j] = 0.0f;
+        if (v < nvec) {
+            unpack8(*reinterpret_cast<const uint4 *>(p.x + t * p.x_stride + v * 8), h[i]);
+            if (p.residual) {
+                float r[8];
+                unpack8(*reinterpret_cast<const uint4 *>(p.residual + t * p.residual_stride + v * 8), r);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) h[i][j] += r[j];
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sum = fmaf(h[i][j], h[i][j], sum);
+    }
+    sum = team_sum<kWide>(sum, part);
+    const float rstd = 1.0f / sqrtf(sum / static_cast<float>(p.hidden) + p.eps);
+    if (p.rstd && lane == 0) p.rstd[t] = rstd;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+        const int v = i * width + lane;
+        if (v < nvec && p.residual_out)
+            *reinterpret_cast<uint4 *>(p.residual_out + t * p.residual_out_stride + v * 8) = pack8(h[i]);
+        float y[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) y[j] = 0.0f;
+        if (v < nvec) {
+            float w[8];
+            load8(p.weight, p.weight_dtype, v * 8, w);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) y[j] = h[i][j] * rstd * w[j];
+            if (p.out) *reinterpret_cast<uint4 *>(p.out + t * p.out_stride + v * 8) = pack8(y);
+        }
+        if (p.values) {
+            // a block of 128 columns is 16 neighbouring lanes (the lanes past the row hold zeros)
+            float m = kFloor;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) m = max_nan(m, fabsf(y[j]));
+#pragma unroll
+            for (int o = 8; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+            if (v < nvec) {
+                const float inv = kFp8Max / m;
+                if ((v & 15) == 0) p.scales[t * p.scale_stride + (v >> 4)] = m * (1.0f / kFp8Max);
+                *reinterpret_cast<uint2 *>(p.values + t * p.value_stride + v * 8) =
+                    make_uint2(pack_fp8x4(y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv),
+                               pack_fp8x4(y[4] * inv, y[5] * inv, y[6] * inv, y[7] * inv));
+            }
+        }
+    }
+}
+
+struct NormGradParams {
+    int64_t tokens;
+    const __nv_bfloat16 *dout, *h, *dresidual;
+    const void *weight;
+    const float *rstd;
+    __nv_bfloat16 *dx;
+    float *part;      // [teams of the grid, hidden] sums of dout * u over a team's rows
+    int64_t dout_stride, h_stride, dresidual_stride, dx_stride;
+    int hidden, weight_dtype;
+};
+
+// A team keeps its columns' sums of dout * u in registers over all its rows
+// (rows team, team + teams, ...) and writes them once; dweight_kernel adds the
+// teams' sums in order.
+template <int VPT, bool kWide>
+__global__ void __launch_bounds__(kWide ? 1024 : 32 * kTeams) norm_grad_kernel(NormGradParams p) {
+    __shared__ float part[2][32];
+    const int64_t team = kWide ? blockIdx.x : static_cast<int64_t>(blockIdx.x) * kTeams + (threadIdx.x >> 5);
+    const int64_t teams = kWide ? gridDim.x : static_cast<int64_t>(gridDim.x) * kTeams;
+    const int lane = kWide ? threadIdx.x : threadIdx.x & 31;
+    const int width = kWide ? blockDim.x : 32;
+    const int nvec = p.hidden >> 3;
+    float dw[VPT][8];
+#pragma unroll
+    for (int i = 0; i < VPT; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) dw[i][j] = 0.0f;
+    int turn = 0;
+    for (int64_t t = team; t < p.tokens; t += teams, turn ^= 1) {
+        const float rstd = p.rstd[t];
+        uint4 d[VPT], s[VPT];
+        float sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const int v = i * width + lane;
+            d[i] = s[i] = make_uint4(0, 0, 0, 0);
+            if (v < nvec) {
+                d[i] = *reinterpret_cast<const uint4 *>(p.dout + t * p.dout_stride + v * 8);
+                s[i] = *reinterpret_cast<const uint4 *>(p.h + t * p.h_stride + v * 8);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const int v = i * width + lane;
+            if (v < nvec) {
+                float g[8], u[8], w[8];
+                unpack8(d[i], g);
+                unpack8(s[i], u);
+                load8(p.weight, p.weight_dtype, v * 8, w);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float gu = g[j] * (u[j] * rstd);
+                    dw[i][j] += gu;
+                    sum = fmaf(gu, w[j], sum);
+                }
+            }
+        }
+        // two rounds of partial sums in turn: a warp that is a row ahead does not write over the last row's
+        const float mean = team_sum<kWide>(sum, part[turn]) / static_cast<float>(p.hidden);
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const int v = i * width + lane;
+            if (v < nvec) {
+                float g[8], u[8], w[8], r[8];
+                unpack8(d[i], g);
+                unpack8(s[i], u);
+                load8(p.weight, p.weight_dtype, v * 8, w);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) r[j] = 0.0f;
+                if (p.dresidual)
+                    unpack8(*reinterpret_cast<const uint4 *>(p.dresidual + t * p.dresidual_stride + v * 8), r);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) r[j] = fmaf(rstd, fmaf(g[j], w[j], -(u[j] * rstd) * mean), r[j]);
+                *reinterpret_cast<uint4 *>(p.dx + t * p.dx_stride + v * 8) = pack8(r);
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+        const int v = i * width + lane;
+        if (v < nvec) {
+            float4 *to = reinterpret_cast<float4 *>(p.part + team * p.hidden + v * 8);
+            to[0] = make_float4(dw[i][0], dw[i][1], dw[i][2], dw[i][3]);
+            to[1] = make_float4(dw[i][4], dw[i][5], dw[i][6], dw[i][7]);
+        }
+    }
+}
+
+// Column sums of part [teams, hidden]: 32 columns to a block, 32 warps that
+// take every 32nd team, then one warp over the warps' sums.
+__global__ void __launch_bounds__(1024) dweight_kernel(const float *part, int teams, int hidden, float *dweight) {
+    __shared__ float sums[32][33];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
+    float s = 0.0f;
+    if (c < hidden)
+        for (int t = warp; t < teams; t += 32) s += part[static_cast<int64_t>(t) * hidden + c];
+    sums[warp][lane] = s;
+    __syncthreads();
+    s = warp_sum(sums[lane][warp]);
+    if (lane == 0 && blockIdx.x * 32 + warp < hidden) dweight[blockIdx.x * 32 + warp] = s;
+}
+
+// How a row is held: VPT steps of 8 columns a lane, and the warps of a block
+// (one warp to a row where wide is false).
+struct Shape {
+    int vpt, warps;
+    bool wide;
+    explicit Shape(int hidden) {
+        const int nvec = hidden / 8;
+        wide = nvec > 128;
+        vpt = nvec > 64 ? 4 : nvec > 32 ? 2 : 1;
+        warps = wide ? (nvec + 127) / 128 : kTeams;
+    }
+    int rows_per_block() const { return wide ? 1 : kTeams; }
+};
+
+// Blocks of the backward kernel: about four a SM where a block is small, so
+// that a team keeps its sums over as many rows as it can.
+int grad_blocks(int64_t tokens, int hidden, int sms) {
+    const Shape s(hidden);
+    const int per_sm = s.warps <= 8 ? 4 : s.warps <= 16 ? 2 : 1;
+    const int64_t rows = (tokens + s.rows_per_block() - 1) / s.rows_per_block();
+    return static_cast<int>(rows < static_cast<int64_t>(sms) * per_sm ? rows : static_cast<int64_t>(sms) * per_sm);
+}
+
+bool rows_ok(const void *p, int64_t stride, int hidden) {
+    return aligned(p, 16) && stride % 8 == 0 && stride >= hidden;
+}
+
+}  // namespace
+
+extern "C" {
+
+ep_status ep_rms_norm(int64_t tokens, int32_t hidden, const void *x, int64_t x_stride, const void *residual,
+                      int64_t residual_stride, const void *weight, int32_t weight_dtype, float eps, void *out,
+                      int64_t out_stride, void *values, int64_t value_stride, float *scales, int64_t scale_stride,
+                      void *residual_out, int64_t residual_out_stride, float *rstd, void *stream) {
+    if (tokens < 0 || tokens >= (1ll << 31) || hidden < 8 || hidden % 8 != 0 || hidden > kMaxHidden)
+        return EP_ERR_INVALID_ARG;
+    if (weight_dtype != EP_DTYPE_F32 && weight_dtype != EP_DTYPE_BF16) return EP_ERR_INVALID_ARG;
+    if (!(eps >= 0.0f)) return EP_ERR_INVALID_ARG;
+    if (tokens == 0) return EP_OK;
+    if (!x || !weight || (!out && !values) || !values != !scales) return EP_ERR_INVALID_ARG;
+    if (!rows_ok(x, x_stride, hidden) || (residual && !rows_ok(residual, residual_stride, hidden)) ||
+        (out && !rows_ok(out, out_stride, hidden)) ||
+        (residual_out && !rows_ok(residual_out, residual_out_stride, hidden)) || !aligned(weight, 16))
+        return EP_ERR_INVALID_ARG;
+    if (values && (!aligned(values, 8) || value_stride % 8 != 0 || value_stride < hidden || !aligned(scales, 4) ||
+                   scale_stride < (hidden + kBlock - 1) / kBlock))
+        return EP_ERR_INVALID_ARG;
+    const Caller c;
+    if (!c.ok) return EP_ERR_CUDA;
+    if (!c.has(x) || !c.has_or_null(residual) || !c.has(weight) || !c.has_or_null(out) || !c.has_or_null(values) ||
+        !c.has_or_null(scales) || !c.has_or_null(residual_out) || !c.has_or_null(rstd))
+        return EP_ERR_INVALID_ARG;
+    NormParams p{};
+    p.tokens = tokens;
+    p.x = static_cast<const __nv_bfloat16 *>(x), p.x_stride = x_stride;
+    p.residual = static_cast<const __nv_bfloat16 *>(residual), p.residual_stride = residual_stride;
+    p.weight = weight, p.weight_dtype = weight_dtype;
+    p.out = static_cast<__nv_bfloat16 *>(out), p.out_stride = out_stride;
+    p.values = static_cast<uint8_t *>(values), p.value_stride = value_stride;
+    p.scales = scales, p.scale_stride = scale_stride;
+    p.residual_out = static_cast<__nv_bfloat16 *>(residual_out), p.residual_out_stride = residual_out_stride;
+    p.rstd = rstd, p.hidden = hidden, p.eps = eps;
+    const Shape s(hidden);
+    const unsigned grid = static_cast<unsigned>((tokens + s.rows_per_block() - 1) / s.rows_per_block());
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (s.wide)
+        norm_kernel<4, true><<<grid, 32 * s.warps, 0, st>>>(p);
+    else if (s.vpt == 4)
+        norm_kernel<4, false><<<grid, 32 * kTeams, 0, st>>>(p);
+    else if (s.vpt == 2)
+        norm_kernel<2, false><<<grid, 32 * kTeams, 0, st>>>(p);
+    else
+        norm_kernel<1, false><<<grid, 32 * kTeams, 0, st>>>(p);
+    return launched();
+}
+
+int64_t ep_rms_norm_backward_workspace(int64_t tokens, int32_t hidden) {
+    if (tokens < 0 || tokens >= (1ll << 31) || hidden < 8 || hidden % 8 != 0 || hidden > kMaxHidden) return 0;
+    // enough for any device: 256 SMs (a grid is cut to what the workspace holds)
+    return static_cast<int64_t>(grad_blocks(tokens, hidden, 256)) * Shape(hidden).rows_per_block() * hidden * 4;
+}
+
+ep_status ep_rms_norm_backward(int64_t tokens, int32_t hidden, const void *dout, int64_t dout_stride, const void *h,
+                               int64_t h_stride, const void *weight, int32_t weight_dtype, const float *rstd,
+                               const void *dresidual, int64_t dresidual_stride, void *dx, int64_t dx_stride,
+                               float *dweight, void *workspace, int64_t workspace_bytes, void *stream) {
+    if (tokens < 0 || tokens >= (1ll << 31) || hidden < 8 || hidden % 8 != 0 || hidden > kMaxHidden)
+        return EP_ERR_INVALID_ARG;
+    if (weight_dtype != EP_DTYPE_F32 && weight_dtype != EP_DTYPE_BF16) return EP_ERR_INVALID_ARG;
+    if (!dweight || !aligned(dweight, 4)) return EP_ERR_INVALID_ARG;
+    const Caller c;
+    if (!c.ok) return EP_ERR_CUDA;
+    if (!c.has(dweight)) return EP_ERR_INVALID_ARG;
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (tokens == 0)
+        return cudaMemsetAsync(dweight, 0, sizeof(float) * hidden, st) == cudaSuccess ? EP_OK : EP_ERR_CUDA;
+    if (!dout || !h || !weight || !rstd || !dx || !workspace ||
+        workspace_bytes < ep_rms_norm_backward_workspace(tokens, hidden))
+        return EP_ERR_INVALID_ARG;
+    if (!rows_ok(dout, dout_stride, hidden) || !rows_ok(h, h_stride, hidden) ||
+        (dresidual && !rows_ok(dresidual, dresidual_stride, hidden)) || !rows_ok(dx, dx_stride, hidden) ||
+        !aligned(weight, 16) || !aligned(rstd, 4) || !aligned(workspace, 16))
+        return EP_ERR_INVALID_ARG;
+    if (!c.has(dout) || !c.has(h) || !c.has(weight) || !c.has(rstd) || !c.has_or_null(dresidual) || !c.has(dx) ||
+        !c.has(workspace))
+        return EP_ERR_INVALID_ARG;
+    const int sms = sm_count_of(c.device);
+    if (sms < 1) return EP_ERR_CUDA;
+    NormGradParams p{};
+    p.tokens = tokens;
+    p.dout = static_cast<const __nv_bfloat16 *>(dout), p.dout_stride = dout_stride;
+    p.h = static_cast<const __nv_bfloat16 *>(h), p.h_stride = h_stride;
+    p.dresidual = static_cast<const __nv_bfloat16 *>(dresidual), p.dresidual_stride = dresidual_stride;
+    p.weight = weight, p.weight_dtype = weight_dtype, p.rstd = rstd;
+    p.dx = static_cast<__nv_bfloat16 *>(dx), p.dx_stride = dx_stride;
+    p.part = static_cast<float *>(workspace), p.hidden = hidden;
+    const Shape s(hidden);
+    const int grid = grad_blocks(tokens, hidden, sms < 256 ? sms : 256);
+    if (s.wide)
+        norm_grad_kernel<4, true><<<grid, 32 * s.warps, 0, st>>>(p);
+    else if (s.vpt == 4)
+        norm_grad_kernel<4, false><<<grid, 32 * kTeams, 0, st>>>(p);
+    else if (s.vpt == 2)
+        norm_grad_kernel<2, false><<<grid, 32 * kTeams, 0, st>>>(p);
+    else
+        norm_grad_kernel<1, false><<<grid, 32 * kTeams, 0, st>>>(p);
+    dweight_kernel<<<(hidden + 31) / 32, 1024, 0, st>>>(p.part, grid * s.rows_per_block(), hidden, dweight);
+    return launched();
+}
+
+}  // extern "C"

@@ -1,0 +1,93 @@
+// ep_ops.cuh -- shared pieces of the operator sources (ep_norm.cu,
+// ep_route.cu, ep_product.cu, ep_picksum.cu): argument checks on the host;
+// bf16 and 8-bit packing, NaN-keeping maxima and row reductions on the device.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp8.h>
+
+#include "ep_internal.cuh"
+#include "ep_ops.h"
+
+namespace ep {
+
+// ------------------------------------------------------------------ host side
+inline bool aligned(const void *p, uintptr_t bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
+
+// The device the calling thread's work goes to, and whether pointers belong to it.
+struct Caller {
+    int device = -1;
+    bool ok;
+    Caller() : ok(cudaGetDevice(&device) == cudaSuccess) {}
+    bool has(const void *p) const { return p != nullptr && ptr_usable_cached(device, p); }
+    bool has_or_null(const void *p) const { return p == nullptr || ptr_usable_cached(device, p); }
+};
+
+// SMs of a device (read once per device; 0 if the runtime does not say).
+inline int sm_count_of(int device) {
+    static int known[64] = {};
+    if (device >= 0 && device < 64 && known[device]) return known[device];
+    int n = 0;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, device) != cudaSuccess) return 0;
+    if (device >= 0 && device < 64) known[device] = n;
+    return n;
+}
+
+inline ep_status launched() { return cudaGetLastError() == cudaSuccess ? EP_OK : EP_ERR_CUDA; }
+
+constexpr int kBlock = 128;                    // columns that share a scale
+constexpr float kFp8Max = 448.0f;              // largest e4m3 value
+constexpr float kFloor = 7.888609052210118e-31f;   // 2^-100: least block maximum of a scale
+
+// ---------------------------------------------------------------- device side
+#ifdef __CUDACC__
+
+__device__ __forceinline__ void unpack2(uint32_t v, float &a, float &b) {
+    a = __uint_as_float(v << 16);
+    b = __uint_as_float(v & 0xffff0000u);
+}
+__device__ __forceinline__ void unpack8(const uint4 &v, float (&f)[8]) {
+    unpack2(v.x, f[0], f[1]);
+    unpack2(v.y, f[2], f[3]);
+    unpack2(v.z, f[4], f[5]);
+    unpack2(v.w, f[6], f[7]);
+}
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+    uint32_t v;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(v) : "f"(b), "f"(a));
+    return v;
+}
+__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
+    return make_uint4(pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7]));
+}
+// four e4m3 values, rounded to nearest even, finite ones kept within +-448
+__device__ __forceinline__ uint32_t pack_fp8x4(float a, float b, float c, float d) {
+    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
+    return lo | (hi << 16);
+}
+// max that gives NaN when either side is NaN
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+// bf16 or fp32 parameter vectors, eight at a time
+__device__ __forceinline__ void load8(const void *p, int dtype, int64_t at, float (&f)[8]) {
+    if (dtype == EP_DTYPE_BF16) {
+        unpack8(__ldg(reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p) + at)), f);
+    } else {
+        const float4 a = __ldg(reinterpret_cast<const float4 *>(static_cast<const float *>(p) + at));
+        const float4 b = __ldg(reinterpret_cast<const float4 *>(static_cast<const float *>(p) + at) + 1);
+        f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+    }
+}
+
+#endif  // __CUDACC__
+
+}  // namespace ep

@@ -1,0 +1,375 @@
+// ep_route.cu -- the router of one layer: softmax, the K largest logits and
+// their weights, per-expert counts and the balance loss, and the logits'
+// gradient (include/ep_ops.h).
+//
+// A warp holds a token's logits in registers, VPT to a lane, expert
+// j * 32 + lane in step j.  Logits are compared as whole numbers in the floats'
+// order, 0 for what is never picked, so that one warp-wide integer maximum
+// finds a pick and one minimum over the lanes' expert ids settles ties.
+#include <type_traits>
+
+#include "ep_ops.cuh"
+
+namespace {
+
+using namespace ep;
+
+constexpr int kMaxExperts = 4096;
+constexpr int kWarps = 8;          // tokens a block works on at once
+
+struct RouteParams {
+    int64_t tokens;
+    const void *logits;
+    int64_t logits_stride;
+    const uint8_t *mask;
+    int32_t *topk_idx;
+    float *topk_weights, *rank_weights, *lse;
+    float *part_p;                 // [grid, experts] sums of p over a block's tokens
+    int32_t *part_count;           // [grid, experts] picks
+    int32_t *part_live;            // [grid] tokens the mask keeps
+    int experts, topk, renormalize, per_rank, bf16;
+};
+
+__device__ __forceinline__ float load_logit(const void *p, int bf16, int64_t at) {
+    return bf16 ? __bfloat162float(static_cast<const __nv_bfloat16 *>(p)[at]) : static_cast<const float *>(p)[at];
+}
+// Whole numbers in the order of the floats; 0 for -inf and NaN, which are
+// never picked (every other float gives more than 0).
+__device__ __forceinline__ uint32_t order_key(float v) {
+    const uint32_t b = __float_as_uint(v + 0.0f);      // -0 and +0 are a tie
+    return v > -INFINITY ? ((b & 0x80000000u) ? ~b : b | 0x80000000u) : 0u;
+}
+__device__ __forceinline__ float key_value(uint32_t k) {
+    return __uint_as_float((k & 0x80000000u) ? k & 0x7fffffffu : ~k);
+}
+
+template <int VPT, bool kTrain>
+__global__ void __launch_bounds__(32 * kWarps) route_kernel(RouteParams p) {
+    extern __shared__ float smem[];      // kTrain: p sums [kWarps][experts], then counts [experts]
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int E = p.experts, K = p.topk;
+    int32_t *count = reinterpret_cast<int32_t *>(smem + (kTrain ? kWarps * E : 0));
+    float psum[kTrain ? VPT : 1];
+    int live_tokens = 0;
+    if (kTrain) {
+        for (int e = threadIdx.x; e < E; e += blockDim.x) count[e] = 0;
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) psum[j] = 0.0f;
+        __syncthreads();
+    }
+    for (int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + warp; t < p.tokens;
+         t += static_cast<int64_t>(gridDim.x) * kWarps) {
+        const bool live = p.mask == nullptr || p.mask[t] != 0;
+        live_tokens += live;
+        float l[VPT];
+        uint32_t best = 0;
+        int best_e = 0;
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            const int e = j * 32 + lane;
+            l[j] = live && e < E ? load_logit(p.logits, p.bf16, t * p.logits_stride + e) : -INFINITY;
+            const uint32_t k = order_key(l[j]);
+            if (k > best) best = k, best_e = e;
+        }
+        const uint32_t top = __reduce_max_sync(0xffffffffu, best);
+        const float most = top ? key_value(top) : 0.0f;
+        float sum = 0.0f;
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) sum += j * 32 + lane < E ? expf(l[j] - most) : 0.0f;
+        sum = warp_sum(sum);       // 0 if no logit is left, NaN if one is NaN
+        // the picks, largest first; lane k keeps pick k
+        uint32_t taken[(VPT + 31) / 32] = {};
+        int my_e = -1;
+        float my_l = -INFINITY;
+        for (int k = 0; k < K; ++k) {
+            const uint32_t m = __reduce_max_sync(0xffffffffu, best);
+            if (m == 0) break;
+            const int e = __reduce_min_sync(0xffffffffu, best == m ? best_e : kMaxExperts);
+            if (lane == k) my_e = e, my_l = key_value(m);
+            if ((e & 31) == lane) {
+                best = 0;
+#pragma unroll
+                for (int j = 0; j < VPT; ++j) {
+                    if (j == e >> 5) taken[j / 32] |= 1u << (j & 31);
+                    const uint32_t key = (taken[j / 32] >> (j & 31)) & 1u ? 0u : order_key(l[j]);
+                    if (key > best) best = key, best_e = j * 32 + lane;
+                }
+            }
+        }
+        float w = my_e >= 0 ? expf(my_l - most) : 0.0f;
+        const float total = p.renormalize ? warp_sum(w) : sum;
+        w = my_e >= 0 ? w / total : 0.0f;
+        if (lane < K) {
+            p.topk_idx[t * K + lane] = my_e;
+            p.topk_weights[t * K + lane] = w;
+        }
+        if (p.rank_weights) {
+            const int rank = my_e >= 0 ? my_e / p.per_rank : -1 - lane;
+            const uint32_t same = __match_any_sync(0xffffffffu, rank);
+            if (lane < K) p.rank_weights[t * K + lane] = my_e >= 0 && __ffs(same) - 1 == lane ? 1.0f : 0.0f;
+        }
+        if (kTrain) {
+            if (my_e >= 0) atomicAdd(&count[my_e], 1);
+            if (lane == 0) p.lse[t] = live ? (top ? most + logf(sum) : sum != sum ? sum : -INFINITY) : INFINITY;
+            const float inv = sum != 0.0f ? 1.0f / sum : 0.0f;
+#pragma unroll
+            for (int j = 0; j < VPT; ++j)
+                if (j * 32 + lane < E) psum[j] += expf(l[j] - most) * inv;
+        }
+    }
+    if (kTrain) {
+#pragma unroll
+        for (int j = 0; j < VPT; ++j)
+            if (j * 32 + lane < E) smem[warp * E + j * 32 + lane] = psum[j];
+        __shared__ int live_of[kWarps];
+        if (lane == 0) live_of[warp] = live_tokens;
+        __syncthreads();
+        for (int e = threadIdx.x; e < E; e += blockDim.x) {
+            float s = 0.0f;
+            for (int w = 0; w < kWarps; ++w) s += smem[w * E + e];
+            p.part_p[static_cast<int64_t>(blockIdx.x) * E + e] = s;
+            p.part_count[static_cast<int64_t>(blockIdx.x) * E + e] = count[e];
+        }
+        if (threadIdx.x == 0) {
+            int s = 0;
+            for (int w = 0; w < kWarps; ++w) s += live_of[w];
+            p.part_live[blockIdx.x] = s;
+        }
+    }
+}
+
+// Adds the blocks' sums in order and makes counts, slope and loss; one block.
+__global__ void __launch_bounds__(1024) balance_kernel(const float *part_p, const int32_t *part_count,
+                                                       const int32_t *part_live, int parts, int experts, int topk,
+                                                       float coef, int32_t *expert_count, float *loss, float *slope) {
+    __shared__ float sums[32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int live = 0;
+    for (int b = 0; b < parts; ++b) live += part_live[b];
+    const float tv = live > 0 ? static_cast<float>(live) : 1.0f;
+    const float scale = coef * static_cast<float>(experts) / (static_cast<float>(topk) * tv * tv);
+    float sum = 0.0f;
+    for (int e = threadIdx.x; e < experts; e += blockDim.x) {
+        float s = 0.0f;
+        int n = 0;
+        for (int b = 0; b < parts; ++b) {
+            s += part_p[static_cast<int64_t>(b) * experts + e];
+            n += part_count[static_cast<int64_t>(b) * experts + e];
+        }
+        const float g = scale * static_cast<float>(n);
+        expert_count[e] = n;
+        slope[e] = g;
+        sum += g * s;
+    }
+    sum = warp_sum(sum);
+    if (lane == 0) sums[warp] = sum;
+    __syncthreads();
+    if (warp == 0) {
+        sum = warp_sum(sums[lane]);
+        if (lane == 0) *loss = sum;
+    }
+}
+
+struct RouteGradParams {
+    int64_t tokens;
+    const void *logits;
+    void *dlogits;
+    const int32_t *topk_idx;
+    const float *topk_weights, *lse, *slope, *dweights, *dloss;
+    int64_t logits_stride, dlogits_stride;
+    int experts, topk, renormalize, bf16;
+};
+
+// dl_e = p_e (g_e - <p, g>) + picks.  Renormalised weights depend on the
+// picked logits alone: a pick's logit gets w (dw - <w, dw>).  Otherwise a
+// weight is its p, and dw joins g.
+template <int VPT>
+__global__ void __launch_bounds__(32 * kWarps) route_grad_kernel(RouteGradParams p) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int E = p.experts, K = p.topk;
+    const int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
+    if (t >= p.tokens) return;
+    const float dloss = p.dloss ? *p.dloss : 0.0f;
+    const float lse = p.lse[t];
+    const bool live = !isinf(lse);       // +inf: a padded token, -inf: no logit left; both have p = 0
+    int idx = -1;
+    float w = 0.0f, add = 0.0f;
+    if (lane < K) {
+        idx = p.topk_idx[t * K + lane];
+        if (idx >= 0) {
+            w = p.topk_weights[t * K + lane];
+            add = p.dweights[t * K + lane];
+        }
+    }
+    if (p.renormalize) {
+        const float mean = warp_sum(w * add);
+        add = w * (add - mean);
+    }
+    float prob[VPT], g[VPT], inner = 0.0f;
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+        const int e = j * 32 + lane;
+        prob[j] = live && e < E ? expf(load_logit(p.logits, p.bf16, t * p.logits_stride + e) - lse) : 0.0f;
+        g[j] = live && e < E && p.dloss ? dloss * p.slope[e] : 0.0f;
+    }
+    if (!p.renormalize)
+        for (int k = 0; k < K; ++k) {
+            const int e = __shfl_sync(0xffffffffu, idx, k);
+            const float a = __shfl_sync(0xffffffffu, add, k);
+#pragma unroll
+            for (int j = 0; j < VPT; ++j)
+                if (e == j * 32 + lane) g[j] += a;
+        }
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) inner = fmaf(prob[j], g[j], inner);
+    inner = warp_sum(inner);
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) g[j] = prob[j] * (g[j] - inner);
+    if (p.renormalize)
+        for (int k = 0; k < K; ++k) {
+            const int e = __shfl_sync(0xffffffffu, idx, k);
+            const float a = __shfl_sync(0xffffffffu, add, k);
+#pragma unroll
+            for (int j = 0; j < VPT; ++j)
+                if (e == j * 32 + lane) g[j] += a;
+        }
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+        const int e = j * 32 + lane;
+        if (e < E) {
+            if (p.bf16)
+                static_cast<__nv_bfloat16 *>(p.dlogits)[t * p.dlogits_stride + e] = __float2bfloat16(g[j]);
+            else
+                static_cast<float *>(p.dlogits)[t * p.dlogits_stride + e] = g[j];
+        }
+    }
+}
+
+int route_blocks(int64_t tokens) {
+    const int64_t want = (tokens + kWarps - 1) / kWarps;
+    return static_cast<int>(want < 304 ? want : 304);
+}
+
+bool sizes_ok(int64_t tokens, int experts, int topk) {
+    return tokens >= 0 && tokens < (1ll << 31) && experts >= 1 && experts <= kMaxExperts && topk >= 1 &&
+           topk <= kMaxTopk && topk <= experts;
+}
+bool logits_ok(const void *p, int dtype, int64_t stride, int experts) {
+    return (dtype == EP_DTYPE_F32 || dtype == EP_DTYPE_BF16) && stride >= experts &&
+           aligned(p, dtype == EP_DTYPE_F32 ? 4 : 2);
+}
+
+template <int VPT>
+void launch_route(const RouteParams &p, bool train, int grid, cudaStream_t st) {
+    const size_t smem = train ? sizeof(float) * p.experts * (kWarps + 1) : 0;
+    if (train) {
+        if (smem > 48 * 1024)
+            (void)cudaFuncSetAttribute(route_kernel<VPT, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       static_cast<int>(smem));
+        route_kernel<VPT, true><<<grid, 32 * kWarps, smem, st>>>(p);
+    } else {
+        route_kernel<VPT, false><<<grid, 32 * kWarps, smem, st>>>(p);
+    }
+}
+
+// Calls f with the number of logits a lane holds, as a type.
+template <typename F>
+void by_width(int experts, F f) {
+    const int v = (experts + 31) / 32;
+    if (v <= 1) f(std::integral_constant<int, 1>());
+    else if (v <= 2) f(std::integral_constant<int, 2>());
+    else if (v <= 4) f(std::integral_constant<int, 4>());
+    else if (v <= 8) f(std::integral_constant<int, 8>());
+    else if (v <= 16) f(std::integral_constant<int, 16>());
+    else if (v <= 32) f(std::integral_constant<int, 32>());
+    else f(std::integral_constant<int, 128>());
+}
+
+}  // namespace
+
+extern "C" {
+
+int64_t ep_route_workspace(int64_t tokens, int32_t experts) {
+    if (!sizes_ok(tokens, experts, 1)) return 0;
+    const int64_t blocks = route_blocks(tokens);
+    return (blocks * (2 * static_cast<int64_t>(experts) + 1)) * 4 + 16;
+}
+
+ep_status ep_route(int64_t tokens, int32_t experts, int32_t topk, const void *logits, int32_t logits_dtype,
+                   int64_t logits_stride, const uint8_t *token_mask, int32_t renormalize, int32_t *topk_idx,
+                   float *topk_weights, int32_t num_ranks, float *rank_weights, float coef, float *lse,
+                   int32_t *expert_count, float *loss, float *slope, void *workspace, int64_t workspace_bytes,
+                   void *stream) {
+    if (!sizes_ok(tokens, experts, topk) || (renormalize != 0 && renormalize != 1)) return EP_ERR_INVALID_ARG;
+    if (num_ranks < 0 || (num_ranks > 0 && experts % num_ranks != 0)) return EP_ERR_INVALID_ARG;
+    const bool train = expert_count != nullptr;
+    if (train != (loss != nullptr) || train != (slope != nullptr) || train != (workspace != nullptr) ||
+        (!train && lse))
+        return EP_ERR_INVALID_ARG;
+    const Caller c;
+    if (!c.ok) return EP_ERR_CUDA;
+    if (train && (workspace_bytes < ep_route_workspace(tokens, experts) || !aligned(workspace, 16) ||
+                  !c.has(expert_count) || !c.has(loss) || !c.has(slope) || !c.has(workspace)))
+        return EP_ERR_INVALID_ARG;
+    if (tokens > 0) {
+        if (!logits || !logits_ok(logits, logits_dtype, logits_stride, experts) || !topk_idx || !topk_weights ||
+            (num_ranks > 0) != (rank_weights != nullptr) || (train && !lse))
+            return EP_ERR_INVALID_ARG;
+        if (!c.has(logits) || !c.has_or_null(token_mask) || !c.has(topk_idx) || !c.has(topk_weights) ||
+            !c.has_or_null(rank_weights) || !c.has_or_null(lse))
+            return EP_ERR_INVALID_ARG;
+    }
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    RouteParams p{};
+    p.tokens = tokens;
+    p.logits = logits, p.logits_stride = logits_stride, p.bf16 = logits_dtype == EP_DTYPE_BF16;
+    p.mask = token_mask, p.topk_idx = topk_idx, p.topk_weights = topk_weights;
+    p.rank_weights = rank_weights, p.lse = lse;
+    p.experts = experts, p.topk = topk, p.renormalize = renormalize;
+    p.per_rank = num_ranks > 0 ? experts / num_ranks : 1;
+    const int blocks = route_blocks(tokens);
+    if (train) {
+        p.part_p = static_cast<float *>(workspace);
+        p.part_count = reinterpret_cast<int32_t *>(p.part_p + static_cast<int64_t>(blocks) * experts);
+        p.part_live = p.part_count + static_cast<int64_t>(blocks) * experts;
+    }
+    if (tokens > 0) {
+        const int grid = train ? blocks : static_cast<int>((tokens + kWarps - 1) / kWarps);
+        by_width(experts, [&](auto v) { launch_route<decltype(v)::value>(p, train, grid, st); });
+    }
+    if (train)
+        balance_kernel<<<1, 1024, 0, st>>>(p.part_p, p.part_count, p.part_live, tokens > 0 ? blocks : 0, experts,
+                                           topk, coef, expert_count, loss, slope);
+    return launched();
+}
+
+ep_status ep_route_backward(int64_t tokens, int32_t experts, int32_t topk, const void *logits, int32_t logits_dtype,
+                            int64_t logits_stride, int32_t renormalize, const int32_t *topk_idx,
+                            const float *topk_weights, const float *lse, const float *slope, const float *dweights,
+                            const float *dloss, void *dlogits, int64_t dlogits_stride, void *stream) {
+    if (!sizes_ok(tokens, experts, topk) || (renormalize != 0 && renormalize != 1)) return EP_ERR_INVALID_ARG;
+    if (tokens == 0) return EP_OK;
+    if (!logits || !logits_ok(logits, logits_dtype, logits_stride, experts) || !dlogits ||
+        !logits_ok(dlogits, logits_dtype, dlogits_stride, experts) || !topk_idx || !topk_weights || !lse || !slope ||
+        !dweights)
+        return EP_ERR_INVALID_ARG;
+    const Caller c;
+    if (!c.ok) return EP_ERR_CUDA;
+    if (!c.has(logits) || !c.has(dlogits) || !c.has(topk_idx) || !c.has(topk_weights) || !c.has(lse) ||
+        !c.has(slope) || !c.has(dweights) || !c.has_or_null(dloss))
+        return EP_ERR_INVALID_ARG;
+    RouteGradParams p{};
+    p.tokens = tokens;
+    p.logits = logits, p.logits_stride = logits_stride, p.bf16 = logits_dtype == EP_DTYPE_BF16;
+    p.dlogits = dlogits, p.dlogits_stride = dlogits_stride;
+    p.topk_idx = topk_idx, p.topk_weights = topk_weights, p.lse = lse, p.slope = slope;
+    p.dweights = dweights, p.dloss = dloss;
+    p.experts = experts, p.topk = topk, p.renormalize = renormalize;
+    const unsigned grid = static_cast<unsigned>((tokens + kWarps - 1) / kWarps);
+    by_width(experts, [&](auto v) {
+        route_grad_kernel<decltype(v)::value><<<grid, 32 * kWarps, 0, static_cast<cudaStream_t>(stream)>>>(p);
+    });
+    return launched();
+}
+
+}  // extern "C"

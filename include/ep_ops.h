@@ -1,0 +1,170 @@
+/*
+ * ep_ops.h -- C ABI of libep's operators around one MoE layer's dispatch and
+ * combine: the residual norm that makes the 8-bit rows a dispatch sends, the
+ * router with its balance loss, the experts' 8-bit products over the
+ * expert-major view of the receive buffer, and the sum of a receive row's
+ * picks that ep_combine reads.
+ *
+ * Conventions (those of ep.h, but no handle is needed):
+ *  - Tensor arguments are DEVICE pointers of the current device, owned by the
+ *    caller.  Each is asked about as ep.h describes; pageable host memory,
+ *    another device's memory and unknown addresses are EP_ERR_INVALID_ARG
+ *    before anything is launched.
+ *  - Matrices are row-major with the columns dense; a row stride is given in
+ *    elements (bytes for 8-bit values, floats for scales).  bf16 rows and
+ *    8-bit rows start on 16-byte boundaries (base and stride).
+ *  - `stream` is a cudaStream_t of the current device; work is enqueued and
+ *    the call returns without waiting.  Nothing is allocated and nothing is
+ *    kept from one call to the next, so calls may run on any streams and
+ *    threads at once as long as their outputs and workspaces are disjoint.
+ *  - Results do not depend on timing: no floating-point atomics.
+ *  - A size of zero rows launches nothing that reads the row pointers, which
+ *    may then be NULL.
+ *
+ * 8-bit rows: float8 e4m3 values with one fp32 scale per block of 128 columns
+ * of a row (the last block may be shorter); a value stands for value * scale.
+ * A block's scale is m / 448 with m = max(|y|) over the block, at least
+ * 2^-100; the values are y * (448 / m) rounded to nearest even.  A block that
+ * holds a NaN has a NaN scale.
+ */
+#ifndef EP_OPS_H_
+#define EP_OPS_H_
+
+#include "ep.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/* Element types of arguments that may come in more than one. */
+#define EP_DTYPE_F32 0
+#define EP_DTYPE_BF16 1
+
+/* ep_rms_norm -- residual addition and root-mean-square norm of T rows:
+ *   h = x + residual (h = x without one);  r = 1 / sqrt(mean(h^2) + eps)
+ *   y = h * r * weight
+ * all in fp32, rounded once per output.
+ *  tokens >= 0; hidden a multiple of 8, 8..32768.
+ *  x, residual: bf16 [tokens, hidden]; residual may be NULL.
+ *  weight: [hidden], weight_dtype EP_DTYPE_BF16 or EP_DTYPE_F32, 16-byte aligned.
+ *  out:    bf16 y, or NULL.
+ *  values, scales: y as 8-bit rows (values 8-byte aligned with a stride that is
+ *          a multiple of 8), or both NULL.  One of out and values is required.
+ *  residual_out: bf16 h, or NULL; may be the residual or x itself.
+ *  rstd:   fp32 [tokens] r, or NULL (ep_rms_norm_backward needs it).
+ * Strides are in elements (bytes for values); hidden if rows are dense. */
+ep_status ep_rms_norm(int64_t tokens, int32_t hidden, const void *x, int64_t x_stride, const void *residual,
+                      int64_t residual_stride, const void *weight, int32_t weight_dtype, float eps, void *out,
+                      int64_t out_stride, void *values, int64_t value_stride, float *scales, int64_t scale_stride,
+                      void *residual_out, int64_t residual_out_stride, float *rstd, void *stream);
+
+/* Bytes of workspace ep_rms_norm_backward needs (host only; 0 if the sizes
+ * are refused). */
+int64_t ep_rms_norm_backward_workspace(int64_t tokens, int32_t hidden);
+
+/* ep_rms_norm_backward -- gradients of ep_rms_norm's bf16 form.  With u = h*r:
+ *   dweight = sum_t dout * u
+ *   dx = dresidual + r * (dout * weight - u * mean(dout * weight * u))
+ * dx is the gradient of x and of residual alike.
+ *  dout, h: bf16 [tokens, hidden]: the output's gradient, and the residual
+ *           stream that the forward call stored.  rstd: fp32 [tokens].
+ *  dresidual: bf16, the gradient that reaches h directly; may be NULL.
+ *  dx: bf16 [tokens, hidden]; may be dout or dresidual itself.
+ *  dweight: fp32 [hidden].
+ *  workspace: at least ep_rms_norm_backward_workspace bytes, 16-byte aligned. */
+ep_status ep_rms_norm_backward(int64_t tokens, int32_t hidden, const void *dout, int64_t dout_stride, const void *h,
+                               int64_t h_stride, const void *weight, int32_t weight_dtype, const float *rstd,
+                               const void *dresidual, int64_t dresidual_stride, void *dx, int64_t dx_stride,
+                               float *dweight, void *workspace, int64_t workspace_bytes, void *stream);
+
+/* ep_route -- the router of one layer: softmax over E logits, the K largest,
+ * their weights; and for training the per-expert counts and the balance loss
+ *   L = coef * sum_e f_e P_e,  f_e = E * count_e / (K * Tv),  P_e = sum_t p[t,e] / Tv
+ * over the Tv tokens that the mask keeps (f is a constant to the gradient).
+ *  experts 1..4096; topk 1..32, at most experts.
+ *  logits: [tokens, experts] fp32 or bf16 (logits_dtype), row stride in elements.
+ *  token_mask: uint8 [tokens], 0 = a padded token: no picks, no part in the
+ *          loss, whatever its logits hold.  NULL: all tokens count.
+ *  renormalize: 1: weights are a softmax over the picked logits; 0: they are
+ *          the picked probabilities.
+ *  topk_idx, topk_weights: int32 and fp32 [tokens, topk], largest first, ties
+ *          to the lower expert.  A logit of -inf or NaN is never picked: where
+ *          fewer than K are left the slot holds -1 and weight 0.  A NaN makes
+ *          its row's probabilities NaN.
+ *  num_ranks, rank_weights: with num_ranks > 0 (a divisor of experts), fp32
+ *          [tokens, topk]: 1 at a token's first pick on each rank, else 0 --
+ *          the weights with which ep_combine adds each rank's row once.
+ *  The rest is for training: all five are given, or all NULL.
+ *  lse:    fp32 [tokens] log of the softmax's sum (+inf for a padded token).
+ *  expert_count: int32 [experts];  loss: fp32 [1];
+ *  slope:  fp32 [experts]: d L / d p[t, e], the same for every kept token.
+ *  workspace: at least ep_route_workspace bytes, 16-byte aligned. */
+ep_status ep_route(int64_t tokens, int32_t experts, int32_t topk, const void *logits, int32_t logits_dtype,
+                   int64_t logits_stride, const uint8_t *token_mask, int32_t renormalize, int32_t *topk_idx,
+                   float *topk_weights, int32_t num_ranks, float *rank_weights, float coef, float *lse,
+                   int32_t *expert_count, float *loss, float *slope, void *workspace, int64_t workspace_bytes,
+                   void *stream);
+int64_t ep_route_workspace(int64_t tokens, int32_t experts);
+
+/* ep_route_backward -- the logits' gradient from the picks' weights' and the
+ * loss's:  dl = p * (g - <p, g>) + the picks' part,  g = dloss * slope.
+ *  logits, topk_idx, topk_weights, lse, slope: as ep_route took and left them.
+ *  dweights: fp32 [tokens, topk]; what stands in a slot without a pick is not used.
+ *  dloss:  fp32 [1] on the device, or NULL for no loss.
+ *  dlogits: [tokens, experts] in the logits' type, row stride in elements; may
+ *          be the logits themselves.  Rows of padded tokens are zero. */
+ep_status ep_route_backward(int64_t tokens, int32_t experts, int32_t topk, const void *logits, int32_t logits_dtype,
+                            int64_t logits_stride, int32_t renormalize, const int32_t *topk_idx,
+                            const float *topk_weights, const float *lse, const float *slope, const float *dweights,
+                            const float *dloss, void *dlogits, int64_t dlogits_stride, void *stream);
+
+/* ep_expert_product -- the experts' products over expert-major places (those
+ * of ep_expert_layout): for expert e and place p in
+ * [expert_off[e], expert_off[e] + expert_count[e])
+ *   y[p, n] = sum_k a[row(p), k] * w[e, n, k],  row(p) = rows[p], or p without rows
+ * of 8-bit rows and 8-bit matrices: each block of 128 columns is multiplied on
+ * the tensor cores and added to fp32 sums with its two scales.
+ *  values, scales: 8-bit rows [a_rows, width]; value_stride a multiple of 16.
+ *  w:        e4m3 [experts, gated ? 2 : 1, out, width], dense, 16-byte aligned.
+ *  w_scales: fp32 [experts, gated ? 2 : 1, ceil(out/128), ceil(width/128)], dense.
+ *  width: a multiple of 16, 16..65536; out: a multiple of 8, 8..65536; experts 1..4096.
+ *  expert_off, expert_count: int32 [experts] on the device.
+ *  rows:     int32 [places], rows of `values`, or NULL (then places <= a_rows).
+ *  gated = 0: y is stored as bf16 [places, out].
+ *  gated = 1: w holds a gate and an up matrix; silu(gate) * up is stored as
+ *          8-bit rows [places, out] in out_values (8-byte aligned, stride a
+ *          multiple of 8) and out_scales.
+ *  Places that no expert holds are not written.  A place outside [0, places)
+ *  is skipped and a row outside [0, a_rows) counts as zeros; both set
+ *  EP_ERR_INVALID_ARG in *status.
+ *  status: device int32, set on such an error and otherwise left alone; may be NULL. */
+ep_status ep_expert_product(int64_t places, int64_t a_rows, int32_t experts, int32_t width, int32_t out,
+                            int32_t gated, const void *values, int64_t value_stride, const float *scales,
+                            int64_t scale_stride, const void *w, const float *w_scales, const int32_t *expert_off,
+                            const int32_t *expert_count, const int32_t *rows, void *out_bf16, int64_t out_stride,
+                            void *out_values, int64_t out_value_stride, float *out_scales,
+                            int64_t out_scale_stride, int32_t *status, void *stream);
+
+/* ep_pick_sum -- one row per receive row from its picks' rows, what ep_combine
+ * reads as expert_out:
+ *   out[r] = bf16_rne(acc), acc = +0; for k with recv_topk_idx[r, k] >= 0:
+ *            acc = fmaf(recv_topk_weights[r, k], y[place(r, k)], acc)
+ * in fp32 and in that order; place(r, k) is the place of row r among its
+ * expert's rows.  A row without picks is zeros.
+ *  recv_topk_idx, recv_topk_weights [rows, topk], expert_rows [places],
+ *  expert_count [experts]: of ep_expert_layout.  recv_base [ranks], expert_off
+ *  [experts]: of ep_layout.  experts is a multiple of ranks; topk 1..32.
+ *  y:   bf16 [places, hidden], out: bf16 [rows, hidden]; hidden a multiple of 8.
+ *  A pick that names no expert of its rank, or a row its expert does not list,
+ *  is skipped and sets EP_ERR_INVALID_ARG in *status.
+ *  status: as in ep_expert_product. */
+ep_status ep_pick_sum(int64_t rows, int64_t places, int32_t hidden, int32_t topk, int32_t ranks, int32_t experts,
+                      const void *y, int64_t y_stride, const int32_t *recv_topk_idx, const float *recv_topk_weights,
+                      const int32_t *recv_base, const int32_t *expert_off, const int32_t *expert_count,
+                      const int32_t *expert_rows, void *out, int64_t out_stride, int32_t *status, void *stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* EP_OPS_H_ */
