@@ -1,6 +1,8 @@
 // ep_product.cu -- the experts' products of 8-bit rows and 8-bit matrices with
 // a scale for each block of 128 columns (rows) and 128 x 128 (matrices), over
 // the expert-major places of the expert layout (include/ep_ops.h).
+#include <cuda.h>
+
 #include "ep_ops.cuh"
 
 namespace {
@@ -18,6 +20,7 @@ struct ProductParams {
     int32_t *status;
     int64_t value_stride, scale_stride, out_stride, out_value_stride, out_scale_stride;
     int experts, width, n, nb, kb;      // n: columns of an output; nb, kb: blocks of 128 in n and width
+    bool wide_out;                      // output rows start on 32-byte boundaries
 };
 
 // Experts' counts as the kernels use them: a segment outside [0, places) is
@@ -31,106 +34,431 @@ __device__ __forceinline__ bool bad_segment(const ProductParams &p, int e) {
     return off < 0 || n < 0 || off + n > p.places;
 }
 
-__device__ __forceinline__ float fp8_value(uint8_t v) {
-    return __half2float(__half(__nv_cvt_fp8_to_halfraw(v, __NV_E4M3)));
+// ------------------------------------------------------------------ tile sizes
+constexpr int kTileM = 128;            // places of a tile
+constexpr int kTileN = 256;            // matrix rows of a tile: 256 columns, or 128 of each matrix of a gated pair
+constexpr int kStages = 4;             // blocks of 128 columns in flight
+constexpr int kABytes = kTileM * kBlock, kBBytes = kTileN * kBlock, kStageBytes = kABytes + kBBytes;
+constexpr int kSums = 8;               // warps that hold the sums
+constexpr int kThreads = 32 * (2 + kSums);
+
+struct Barriers {
+    uint64_t full[kStages], empty[kStages];      // a stage has landed / has been multiplied
+    uint64_t tfull[2], tempty[2];                // an accumulator is complete / has been read
+    uint64_t pair[4];                            // both halves of 32 rows have their maxima
+};
+
+struct Tile {
+    int expert, m0, here, n;       // first place within the expert, places of the tile, column tile
+    int64_t first;                 // its first place
+};
+
+// Wait of a whole warp with a limit; the first one to run out ends the others'
+// waits.  The answer is the same for every lane.
+__device__ __forceinline__ bool wait_for(uint64_t *bar, uint32_t parity, volatile int *stop) {
+    if (__all_sync(0xffffffffu, mbar_try(bar, parity))) return true;
+    const uint64_t t0 = globaltimer_ns();
+    while (!__all_sync(0xffffffffu, mbar_try(bar, parity))) {
+        if (__any_sync(0xffffffffu, *stop != 0 || globaltimer_ns() - t0 > kDefaultTimeoutNs)) {
+            *stop = 1;
+            return false;
+        }
+    }
+    return true;
 }
 
-constexpr int kM = 32, kK = 32;
+// ---- tensor maps, tensor cores and their memory (PTX)
+__device__ __forceinline__ void load_4d(void *dst, const CUtensorMap *map, int x, int y, int z, int w, uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(
+            smem_u32(dst)),
+        "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
+        : "memory");
+}
+__device__ __forceinline__ void load_2d(void *dst, const CUtensorMap *map, int x, int y, uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+            smem_u32(dst)),
+        "l"(map), "r"(x), "r"(y), "r"(smem_u32(bar))
+        : "memory");
+}
+__device__ __forceinline__ void load_rows4(void *dst, const CUtensorMap *map, int x, const int (&y)[4], uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cta.global.tile::gather4.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(smem_u32(dst)),
+        "l"(map), "r"(x), "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3]), "r"(smem_u32(bar))
+        : "memory");
+}
+__device__ __forceinline__ bool elected() {
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok));
+    return ok != 0;
+}
+// Operand in shared memory, rows of 128 bytes in the 128-byte swizzle: 8-row
+// groups 1024 bytes apart, 16-byte units, format version 1.
+__device__ __forceinline__ uint64_t operand(const void *p) {
+    return (static_cast<uint64_t>(smem_u32(p)) >> 4) | (1ull << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
+}
+// e4m3 x e4m3 -> fp32, both operands with dense columns, kTileM x kTileN.
+constexpr uint32_t kShape = (1u << 4) | (static_cast<uint32_t>(kTileN >> 3) << 17) | (static_cast<uint32_t>(kTileM >> 4) << 24);
 
-// 32 places x 128 columns a block (of both matrices where kGated), fp32
-// products of 32 columns at a time through shared memory.  A warp holds four
-// places, a lane four columns of each, so that a place's block maximum is one
-// warp's.
-template <bool kGated>
-__global__ void __launch_bounds__(256) product_kernel(ProductParams p) {
-    __shared__ float a[kM][kK + 1], b[kGated ? 2 : 1][kBlock][kK + 1];
-    __shared__ int s_expert, s_tile;
+__device__ __forceinline__ void multiply(uint32_t acc, uint64_t a, uint64_t b, bool add) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(acc),
+        "l"(a), "l"(b), "r"(kShape), "r"(static_cast<uint32_t>(add))
+        : "memory");
+}
+__device__ __forceinline__ void commit(uint64_t *bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
+                 : "memory");
+}
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+// 32 columns of the thread's row of an accumulator
+__device__ __forceinline__ void read32(uint32_t at, float (&v)[32]) {
+    uint32_t r[32];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, "
+        "%23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(at)
+        : "memory");
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// 32 bytes to one row, in one store where rows start on 32-byte boundaries.
+__device__ __forceinline__ void store32(void *to, const uint32_t (&v)[8], bool wide) {
+    if (wide) {
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(v[0]), "r"(v[1]),
+                     "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                     : "memory");
+    } else {
+        // rows start on 8-byte boundaries at least
+#pragma unroll
+        for (int i = 0; i < 4; ++i) static_cast<uint2 *>(to)[i] = make_uint2(v[2 * i], v[2 * i + 1]);
+    }
+}
+
+// Tiles in the order expert, column tile, place tile (place tiles next to each
+// other, so that CTAs that run together share a matrix tile and an expert's
+// rows in L2).  start[e] = tiles before expert e, start[experts] = all.
+__device__ __forceinline__ bool tile_of(const ProductParams &p, const int *start, int ntiles, int id, Tile &t) {
+    if (id >= start[p.experts]) return false;
+    int lo = 0, hi = p.experts;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (start[mid] <= id) lo = mid;
+        else hi = mid;
+    }
+    const int count = count_of(p, lo), mtiles = (count + kTileM - 1) / kTileM, at = id - start[lo];
+    t.expert = lo;
+    t.n = at / mtiles;
+    t.m0 = (at - t.n * mtiles) * kTileM;
+    t.here = min(kTileM, count - t.m0);
+    t.first = p.expert_off[lo] + static_cast<int64_t>(t.m0);
+    return true;
+}
+
+template <bool kGated, bool kGather>
+__global__ void __launch_bounds__(kThreads, 1)
+    product_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap wmap,
+                   const __grid_constant__ ProductParams p) {
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ Barriers bar;
+    __shared__ uint32_t s_tmem;
+    __shared__ int s_stop, s_scan[kThreads / 32];
+    __shared__ float s_most[2][2][kTileM];      // by turn, half, row
+    uint8_t *stages = smem_raw + (-smem_u32(smem_raw) & 1023u);
+    int *start = reinterpret_cast<int *>(stages + kStages * kStageBytes);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int ntiles = (p.n + (kGated ? kBlock : kTileN) - 1) / (kGated ? kBlock : kTileN);
+
     if (tid == 0) {
-        int left = blockIdx.y, e = 0;
-        for (; e < p.experts; ++e) {
-            const int tiles = (count_of(p, e) + kM - 1) / kM;
-            if (bad_segment(p, e) && p.status) set_error(p.status, EP_ERR_INVALID_ARG);
-            if (left < tiles) break;
-            left -= tiles;
-        }
-        s_expert = e;
-        s_tile = left;
+        for (int i = 0; i < kStages; ++i) mbar_init(&bar.full[i], 1), mbar_init(&bar.empty[i], 1);
+        for (int i = 0; i < 2; ++i) mbar_init(&bar.tfull[i], 1), mbar_init(&bar.tempty[i], kSums);
+        for (int i = 0; i < 4; ++i) mbar_init(&bar.pair[i], 2);
+        mbar_fence_init();
+        s_stop = 0;
     }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&s_tmem)) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+    // tiles before each expert
+    int carry = 0;
+    for (int e0 = 0; e0 < p.experts; e0 += kThreads) {
+        const int e = e0 + tid;
+        int own = 0;
+        if (e < p.experts) {
+            own = (count_of(p, e) + kTileM - 1) / kTileM * ntiles;
+            if (blockIdx.x == 0 && p.status && bad_segment(p, e)) set_error(p.status, EP_ERR_INVALID_ARG);
+        }
+        int incl = own;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += v;
+        }
+        if (lane == 31) s_scan[warp] = incl;
+        __syncthreads();
+        int before = carry, all = 0;
+        for (int w = 0; w < kThreads / 32; ++w) {
+            if (w < warp) before += s_scan[w];
+            all += s_scan[w];
+        }
+        if (e < p.experts) start[e] = before + incl - own;
+        carry += all;
+        __syncthreads();
+    }
+    if (tid == 0) start[p.experts] = carry;
+    fence_before();
     __syncthreads();
-    const int e = s_expert;
-    if (e >= p.experts) return;
-    const int n0 = blockIdx.x * kBlock;
-    const int64_t first = p.expert_off[e] + static_cast<int64_t>(s_tile) * kM;
-    const int here = min(kM, count_of(p, e) - s_tile * kM);
-    float acc[kGated ? 2 : 1][4][4] = {};
-    for (int k0 = 0; k0 < p.width; k0 += kK) {
-        const int block = k0 / kBlock;
-        for (int i = tid; i < kM * kK; i += 256) {
-            const int m = i / kK, k = k0 + i % kK;
-            float v = 0.0f;
-            if (m < here && k < p.width) {
-                const int64_t row = p.rows ? p.rows[first + m] : first + m;
-                if (row >= 0 && row < p.a_rows)
-                    v = fp8_value(p.values[row * p.value_stride + k]) * p.scales[row * p.scale_stride + block];
-                else if (p.status)
-                    set_error(p.status, EP_ERR_INVALID_ARG);
-            }
-            a[m][i % kK] = v;
-        }
+    fence_after();
+    const uint32_t tmem = s_tmem;
+    Tile t;
+
+    if (warp == 0) {
+        // ---- loads: the tile's rows and matrix rows, 128 columns at a time
+        int stage = 0;
+        uint32_t phase = 0;
+        for (int id = blockIdx.x; tile_of(p, start, ntiles, id, t); id += gridDim.x) {
+            int y[4] = {};
+            if (kGather) {
 #pragma unroll
-        for (int h = 0; h < (kGated ? 2 : 1); ++h) {
-            const int64_t matrix = static_cast<int64_t>(e) * (kGated ? 2 : 1) + h;
-            const float s = p.w_scales[(matrix * p.nb + blockIdx.x) * p.kb + block];
-            for (int i = tid; i < kBlock * kK; i += 256) {
-                const int n = n0 + i / kK, k = k0 + i % kK;
-                b[h][i / kK][i % kK] =
-                    n < p.n && k < p.width ? fp8_value(p.w[(matrix * p.n + n) * p.width + k]) * s : 0.0f;
-            }
-        }
-        __syncthreads();
-#pragma unroll 4
-        for (int k = 0; k < kK; ++k) {
-            float x[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) x[i] = a[warp * 4 + i][k];
-#pragma unroll
-            for (int h = 0; h < (kGated ? 2 : 1); ++h)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float y = b[h][j * 32 + lane][k];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) acc[h][i][j] = fmaf(x[i], y, acc[h][i][j]);
+                for (int i = 0; i < 4; ++i) {
+                    const int m = 4 * lane + i;
+                    if (m < t.here) y[i] = p.rows[t.first + m];
+                    if (y[i] < 0 || y[i] >= p.a_rows) y[i] = 0;      // its sums are not used
                 }
+            }
+            const int pieces = kGather ? (t.here + 3) / 4 : (t.here + 31) / 32;
+            const uint32_t bytes = kBBytes + pieces * (kGather ? 4 : 32) * kBlock;
+            for (int kb = 0; kb < p.kb; ++kb) {
+                if (!wait_for(&bar.empty[stage], phase ^ 1u, &s_stop)) goto done;
+                uint8_t *a = stages + stage * kStageBytes;
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(&bar.full[stage], bytes);
+                    load_4d(a + kABytes, &wmap, kb * kBlock, t.n * (kGated ? kBlock : kTileN), 0, t.expert,
+                            &bar.full[stage]);
+                }
+                __syncwarp();
+                if (lane < pieces) {
+                    if (kGather) load_rows4(a + lane * 4 * kBlock, &amap, kb * kBlock, y, &bar.full[stage]);
+                    else load_2d(a + lane * 32 * kBlock, &amap, kb * kBlock, static_cast<int>(t.first) + lane * 32, &bar.full[stage]);
+                }
+                __syncwarp();
+                if (++stage == kStages) stage = 0, phase ^= 1u;
+            }
+        }
+        // let what is in flight land: every stage that was filled is emptied by the multiplier
+        for (int i = 0; i < kStages; ++i) {
+            if (!wait_for(&bar.empty[stage], phase ^ 1u, &s_stop)) break;
+            if (++stage == kStages) stage = 0, phase ^= 1u;
+        }
+    } else if (warp == 1) {
+        // ---- products: one block of 128 columns into one of two accumulators
+        int stage = 0, buf = 0;
+        uint32_t phase = 0, tphase = 0;
+        for (int id = blockIdx.x; tile_of(p, start, ntiles, id, t); id += gridDim.x) {
+            for (int kb = 0; kb < p.kb; ++kb) {
+                if (!wait_for(&bar.tempty[buf], tphase ^ 1u, &s_stop)) goto done;
+                if (!wait_for(&bar.full[stage], phase, &s_stop)) goto done;
+                fence_after();
+                if (elected()) {
+                    const uint64_t a = operand(stages + stage * kStageBytes);
+                    const uint64_t b = operand(stages + stage * kStageBytes + kABytes);
+#pragma unroll
+                    for (int k = 0; k < kBlock / 32; ++k)       // 32 columns an instruction: 2 units of 16 bytes
+                        multiply(tmem + buf * kTileN, a + 2 * k, b + 2 * k, k > 0);
+                    commit(&bar.empty[stage]);
+                    commit(&bar.tfull[buf]);
+                }
+                __syncwarp();
+                if (++stage == kStages) stage = 0, phase ^= 1u;
+                buf ^= 1;
+                if (buf == 0) tphase ^= 1u;
+            }
+        }
+    } else {
+        // ---- sums: accumulator times the two scales, added up in registers.
+        // A warp reads the 32 rows that its number allows, and half the columns:
+        // one block of 128, or 64 of the gate's and the same 64 of the up matrix's.
+        const int quad = warp & 3, half = (warp - 2) >> 2, row = quad * 32 + lane;
+        int buf = 0, turn = 0;
+        uint32_t tphase = 0;
+        for (int id = blockIdx.x; tile_of(p, start, ntiles, id, t); id += gridDim.x) {
+            const int block = kGated ? t.n : t.n * 2 + half;
+            const bool active = quad * 32 < t.here && block < p.nb;
+            const bool mine = row < t.here;
+            int64_t src = -1;
+            if (mine) {
+                src = kGather ? p.rows[t.first + row] : t.first + row;
+                if (src < 0 || src >= p.a_rows) {
+                    src = -1;
+                    if (p.status) set_error(p.status, EP_ERR_INVALID_ARG);
+                }
+            }
+            const float *sa = p.scales + (src < 0 ? 0 : src * p.scale_stride);
+            const float *sw = p.w_scales + (static_cast<int64_t>(t.expert) * (kGated ? 2 : 1) * p.nb + (active ? block : 0)) * p.kb;
+            float acc[128];
+#pragma unroll
+            for (int i = 0; i < 128; ++i) acc[i] = 0.0f;
+            for (int kb = 0; kb < p.kb; ++kb) {
+                const float x = src < 0 ? 0.0f : sa[kb];
+                const float s0 = x * sw[kb], s1 = kGated ? x * sw[static_cast<int64_t>(p.nb) * p.kb + kb] : s0;
+                if (!wait_for(&bar.tfull[buf], tphase, &s_stop)) goto done;
+                fence_after();
+                if (active) {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        float v[32];
+                        const int col = kGated ? (c >> 1) * 128 + half * 64 + (c & 1) * 32 : half * 128 + c * 32;
+                        read32(tmem + (static_cast<uint32_t>(quad * 32) << 16) + buf * kTileN + col, v);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) acc[c * 32 + i] = fmaf(v[i], c < 2 ? s0 : s1, acc[c * 32 + i]);
+                    }
+                }
+                fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar.tempty[buf]);
+                buf ^= 1;
+                if (buf == 0) tphase ^= 1u;
+            }
+            if (kGated) {
+                float most = kFloor;
+#pragma unroll
+                for (int i = 0; i < 64; ++i) {
+                    const float g = acc[i];
+                    const int col = t.n * kBlock + half * 64 + i;
+                    acc[i] = src >= 0 && col < p.n ? g / (1.0f + expf(-g)) * acc[64 + i] : 0.0f;
+                    most = max_nan(most, fabsf(acc[i]));
+                }
+                // the other half's maximum; two turns, as a warp may be a tile ahead when the other one reads
+                s_most[turn][half][row] = most;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar.pair[quad]);
+                if (!wait_for(&bar.pair[quad], turn, &s_stop)) goto done;
+                most = max_nan(most, s_most[turn][half ^ 1][row]);
+                turn ^= 1;
+                if (mine) {
+                    const float inv = kFp8Max / most;
+                    if (half == 0) p.out_scales[(t.first + row) * p.out_scale_stride + t.n] = most * (1.0f / kFp8Max);
+                    uint8_t *to = p.out_values + (t.first + row) * p.out_value_stride + t.n * kBlock + half * 64;
+                    const int left = p.n - (t.n * kBlock + half * 64);
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        uint32_t v[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const float *f = acc + c * 32 + i * 4;
+                            v[i] = pack_fp8x4(f[0] * inv, f[1] * inv, f[2] * inv, f[3] * inv);
+                        }
+                        if (left >= c * 32 + 32) {
+                            store32(to + c * 32, v, p.wide_out);
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                if (left >= c * 32 + i * 8 + 8)
+                                    *reinterpret_cast<uint2 *>(to + c * 32 + i * 8) = make_uint2(v[2 * i], v[2 * i + 1]);
+                        }
+                    }
+                }
+            } else if (mine && active) {
+                __nv_bfloat16 *to = p.out + (t.first + row) * p.out_stride + block * kBlock;
+                const int left = p.n - block * kBlock;
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                    uint32_t v[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        v[i] = src < 0 ? 0u : pack2(acc[c * 16 + 2 * i], acc[c * 16 + 2 * i + 1]);
+                    if (left >= c * 16 + 16) {
+                        store32(to + c * 16, v, p.wide_out);
+                    } else if (left >= c * 16 + 8) {
+                        *reinterpret_cast<uint4 *>(to + c * 16) = make_uint4(v[0], v[1], v[2], v[3]);
+                    }
+                }
+            }
+        }
+    }
+done:
+    __syncwarp();
+    fence_before();
+    __syncthreads();
+    if (s_stop) {
+        // a wait ran out: the copies that were started still write to this block's memory
+        if (p.status && tid == 0) set_error(p.status, EP_ERR_TIMEOUT);
+        const uint64_t t0 = globaltimer_ns();
+        while (globaltimer_ns() - t0 < 1000000ull) {
         }
         __syncthreads();
     }
-    for (int i = 0; i < 4; ++i) {
-        const int m = warp * 4 + i;
-        if (m >= here) break;
-        if (!kGated) {
-            for (int j = 0; j < 4; ++j) {
-                const int n = n0 + j * 32 + lane;
-                if (n < p.n) p.out[(first + m) * p.out_stride + n] = __float2bfloat16(acc[0][i][j]);
-            }
-        } else {
-            float y[4], most = kFloor;
-            for (int j = 0; j < 4; ++j) {
-                const float g = acc[0][i][j];
-                y[j] = n0 + j * 32 + lane < p.n ? g / (1.0f + expf(-g)) * acc[kGated ? 1 : 0][i][j] : 0.0f;
-                most = max_nan(most, fabsf(y[j]));
-            }
-            for (int o = 16; o > 0; o >>= 1) most = max_nan(most, __shfl_xor_sync(0xffffffffu, most, o));
-            const float inv = kFp8Max / most;
-            if (lane == 0) p.out_scales[(first + m) * p.out_scale_stride + blockIdx.x] = most * (1.0f / kFp8Max);
-            for (int j = 0; j < 4; ++j) {
-                const int n = n0 + j * 32 + lane;
-                if (n < p.n)
-                    p.out_values[(first + m) * p.out_value_stride + n] =
-                        __nv_cvt_float_to_fp8(y[j] * inv, __NV_SATFINITE, __NV_E4M3);
-            }
-        }
+    if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+}
+
+// ------------------------------------------------------------------ host side
+using EncodeFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                              const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                              CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeFn encoder() {
+    static const EncodeFn fn = [] {
+        void *f = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            f = nullptr;
+        return reinterpret_cast<EncodeFn>(f);
+    }();
+    return fn;
+}
+
+bool encode(CUtensorMap *map, const void *base, int rank, const cuuint64_t *dims, const cuuint64_t *strides,
+            const cuuint32_t *box) {
+    const cuuint32_t ones[4] = {1, 1, 1, 1};
+    const EncodeFn fn = encoder();
+    return fn && fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, rank, const_cast<void *>(base), dims, strides, box, ones,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <bool kGated, bool kGather>
+ep_status launch_product(const ProductParams &p, int device, cudaStream_t st) {
+    const int sms = sm_count_of(device);
+    if (sms < 1) return EP_ERR_CUDA;
+    CUtensorMap amap, wmap;
+    // without rows to read (every place's row is then out of range) any readable row will do
+    const cuuint64_t adims[2] = {static_cast<cuuint64_t>(p.width), static_cast<cuuint64_t>(p.a_rows ? p.a_rows : 1)};
+    const cuuint64_t astride[1] = {static_cast<cuuint64_t>(p.a_rows ? p.value_stride : p.width)};
+    const cuuint32_t abox[2] = {kBlock, kGather ? 1u : 32u};
+    const cuuint64_t wdims[4] = {static_cast<cuuint64_t>(p.width), static_cast<cuuint64_t>(p.n), kGated ? 2u : 1u,
+                                 static_cast<cuuint64_t>(p.experts)};
+    const cuuint64_t matrix = static_cast<cuuint64_t>(p.width) * p.n;
+    const cuuint64_t wstride[3] = {static_cast<cuuint64_t>(p.width), matrix, matrix * (kGated ? 2 : 1)};
+    const cuuint32_t wbox[4] = {kBlock, static_cast<cuuint32_t>(kGated ? kBlock : kTileN), kGated ? 2u : 1u, 1};
+    if (!encode(&amap, p.a_rows ? p.values : p.w, 2, adims, astride, abox) || !encode(&wmap, p.w, 4, wdims, wstride, wbox))
+        return EP_ERR_CUDA;
+    const size_t smem = 1024 + kStages * kStageBytes + sizeof(int) * (p.experts + 1);
+    static bool ready[64] = {};
+    if (device >= 64 || !ready[device]) {
+        if (cudaFuncSetAttribute(product_kernel<kGated, kGather>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 1024 + kStages * kStageBytes + 4 * 4097) != cudaSuccess)
+            return EP_ERR_CUDA;
+        if (device < 64) ready[device] = true;
     }
+    const int64_t ntiles = (p.n + (kGated ? kBlock : kTileN) - 1) / (kGated ? kBlock : kTileN);
+    // every expert may leave one tile short
+    const int64_t tiles = (p.places / kTileM + (p.places < p.experts ? p.places : p.experts)) * ntiles;
+    const unsigned grid = static_cast<unsigned>(tiles < sms ? tiles : sms);
+    product_kernel<kGated, kGather><<<grid, kThreads, smem, st>>>(amap, wmap, p);
+    return launched();
 }
 
 }  // namespace
@@ -175,13 +503,11 @@ extern "C" ep_status ep_expert_product(int64_t places, int64_t a_rows, int32_t e
     p.out_scales = out_scales, p.out_scale_stride = out_scale_stride;
     p.status = status;
     p.experts = experts, p.width = width, p.n = out, p.nb = nb, p.kb = kb;
-    // every expert may leave one tile short
-    const int64_t tiles = places / kM + (places < experts ? places : experts);
-    if (tiles > 65535) return EP_ERR_INVALID_ARG;
-    const dim3 grid(nb, static_cast<unsigned>(tiles));
-    if (gated)
-        product_kernel<true><<<grid, 256, 0, static_cast<cudaStream_t>(stream)>>>(p);
-    else
-        product_kernel<false><<<grid, 256, 0, static_cast<cudaStream_t>(stream)>>>(p);
-    return launched();
+    p.wide_out = gated ? aligned(out_values, 32) && out_value_stride % 32 == 0
+                       : aligned(out_bf16, 32) && out_stride % 16 == 0;
+    // tiles are counted in 32 bits
+    if ((places / kTileM + experts) * nb >= (1ll << 31)) return EP_ERR_INVALID_ARG;
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (gated) return rows ? launch_product<true, true>(p, c.device, st) : launch_product<true, false>(p, c.device, st);
+    return rows ? launch_product<false, true>(p, c.device, st) : launch_product<false, false>(p, c.device, st);
 }
