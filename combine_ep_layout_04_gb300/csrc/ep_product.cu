@@ -20,7 +20,7 @@ struct ProductParams {
     int32_t *status;
     int64_t value_stride, scale_stride, out_stride, out_value_stride, out_scale_stride;
     int experts, width, n, nb, kb;      // n: columns of an output; nb, kb: blocks of 128 in n and width
-    bool wide_out;                      // output rows start on 32-byte boundaries
+    bool wide_out, wide_scales;         // output rows start on 32-byte boundaries, rows of scales on 16-byte ones
 };
 
 // Experts' counts as the kernels use them: a segment outside [0, places) is
@@ -39,8 +39,14 @@ constexpr int kTileM = 128;            // places of a tile
 constexpr int kTileN = 256;            // matrix rows of a tile: 256 columns, or 128 of each matrix of a gated pair
 constexpr int kStages = 4;             // blocks of 128 columns in flight
 constexpr int kABytes = kTileM * kBlock, kBBytes = kTileN * kBlock, kStageBytes = kABytes + kBBytes;
-constexpr int kSums = 8;               // warps that hold the sums
-constexpr int kThreads = 32 * (2 + kSums);
+constexpr int kSums = 8;               // warps that hold the sums: two warpgroups
+constexpr int kGatherWarps = 2;        // warps that fetch rows one by one
+constexpr int kGatherLag = 2;          // blocks of 128 columns a gathering thread has in flight
+constexpr int kThreads = 32 * (4 + kSums);
+// Registers: a sums thread holds 128 fp32 sums; the first warpgroup gives up
+// what it does not need (the two shares are the launch's 168 a thread).
+constexpr int kFewRegs = 72, kManyRegs = 216;
+static_assert(128 * kFewRegs + 256 * kManyRegs <= kThreads * 168, "register shares exceed the launch's");
 
 struct Barriers {
     uint64_t full[kStages], empty[kStages];      // a stage has landed / has been multiplied
@@ -82,12 +88,9 @@ __device__ __forceinline__ void load_2d(void *dst, const CUtensorMap *map, int x
         "l"(map), "r"(x), "r"(y), "r"(smem_u32(bar))
         : "memory");
 }
-__device__ __forceinline__ void load_rows4(void *dst, const CUtensorMap *map, int x, const int (&y)[4], uint64_t *bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cta.global.tile::gather4.mbarrier::complete_tx::bytes "
-        "[%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(smem_u32(dst)),
-        "l"(map), "r"(x), "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3]), "r"(smem_u32(bar))
-        : "memory");
+// 16 bytes, or zeros without a source
+__device__ __forceinline__ void fetch16(uint32_t dst, const void *src, bool there) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
 }
 __device__ __forceinline__ bool elected() {
     uint32_t ok;
@@ -115,23 +118,32 @@ __device__ __forceinline__ void commit(uint64_t *bar) {
 }
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-// 32 columns of the thread's row of an accumulator
-__device__ __forceinline__ void read32(uint32_t at, float (&v)[32]) {
-    uint32_t r[32];
+// 16 columns of the thread's row of an accumulator, as pairs; complete after
+// landed(), which the pairs pass through so that no use moves before it.
+__device__ __forceinline__ void read16(uint32_t at, uint32_t (&r)[16]) {
     asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, "
-        "%23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
         : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
-          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
         : "r"(at)
         : "memory");
-    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
+__device__ __forceinline__ void landed(uint32_t (&r)[16]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+                 :
+                 : "memory");
+}
+// sums of two neighbouring columns: acc += v * s
+__device__ __forceinline__ void add_pair(unsigned long long &acc, uint32_t v0, uint32_t v1, float s) {
+    asm("{\n\t.reg .b64 v, s;\n\tmov.b64 v, {%1, %2};\n\tmov.b64 s, {%3, %3};\n\tfma.rn.f32x2 %0, v, s, %0;\n\t}"
+        : "+l"(acc)
+        : "r"(v0), "r"(v1), "r"(__float_as_uint(s)));
+}
+__device__ __forceinline__ float low_of(unsigned long long v) { return __uint_as_float(static_cast<uint32_t>(v)); }
+__device__ __forceinline__ float high_of(unsigned long long v) { return __uint_as_float(static_cast<uint32_t>(v >> 32)); }
 
 // 32 bytes to one row, in one store where rows start on 32-byte boundaries.
 __device__ __forceinline__ void store32(void *to, const uint32_t (&v)[8], bool wide) {
@@ -181,7 +193,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int ntiles = (p.n + (kGated ? kBlock : kTileN) - 1) / (kGated ? kBlock : kTileN);
 
     if (tid == 0) {
-        for (int i = 0; i < kStages; ++i) mbar_init(&bar.full[i], 1), mbar_init(&bar.empty[i], 1);
+        for (int i = 0; i < kStages; ++i)
+            mbar_init(&bar.full[i], kGather ? 1 + kGatherWarps : 1), mbar_init(&bar.empty[i], 1);
         for (int i = 0; i < 2; ++i) mbar_init(&bar.tfull[i], 1), mbar_init(&bar.tempty[i], kSums);
         for (int i = 0; i < 4; ++i) mbar_init(&bar.pair[i], 2);
         mbar_fence_init();
@@ -222,123 +235,219 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     fence_after();
     const uint32_t tmem = s_tmem;
-    Tile t;
-
-    if (warp == 0) {
-        // ---- loads: the tile's rows and matrix rows, 128 columns at a time
+    if (warp < 4) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFewRegs));
+        Tile t;
         int stage = 0;
         uint32_t phase = 0;
-        for (int id = blockIdx.x; tile_of(p, start, ntiles, id, t); id += gridDim.x) {
-            int y[4] = {};
-            if (kGather) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int m = 4 * lane + i;
-                    if (m < t.here) y[i] = p.rows[t.first + m];
-                    if (y[i] < 0 || y[i] >= p.a_rows) y[i] = 0;      // its sums are not used
+        if (warp == 0) {
+            // ---- loads: matrix rows, and places' rows where they lie in order, 128 columns at a time
+            for (int id = blockIdx.x; tile_of(p, start, ntiles, id, t); id += gridDim.x) {
+                const int pieces = kGather ? 0 : (t.here + 31) / 32;
+                for (int kb = 0; kb < p.kb; ++kb) {
+                    if (!wait_for(&bar.empty[stage], phase ^ 1u, &s_stop)) goto done;
+                    uint8_t *a = stages + stage * kStageBytes;
+                    if (lane == 0) {
+                        mbar_arrive_expect_tx(&bar.full[stage], kBBytes + pieces * 32 * kBlock);
+                        load_4d(a + kABytes, &wmap, kb * kBlock, t.n * (kGated ? kBlock : kTileN), 0, t.expert,
+                                &bar.full[stage]);
+                    }
+                    __syncwarp();
+                    if (!kGather && lane < pieces)
+                        load_2d(a + lane * 32 * kBlock, &amap, kb * kBlock, static_cast<int>(t.first) + lane * 32,
+                                &bar.full[stage]);
+                    __syncwarp();
+                    if (++stage == kStages) stage = 0, phase ^= 1u;
                 }
             }
-            const int pieces = kGather ? (t.here + 3) / 4 : (t.here + 31) / 32;
-            const uint32_t bytes = kBBytes + pieces * (kGather ? 4 : 32) * kBlock;
-            for (int kb = 0; kb < p.kb; ++kb) {
-                if (!wait_for(&bar.empty[stage], phase ^ 1u, &s_stop)) goto done;
-                uint8_t *a = stages + stage * kStageBytes;
-                if (lane == 0) {
-                    mbar_arrive_expect_tx(&bar.full[stage], bytes);
-                    load_4d(a + kABytes, &wmap, kb * kBlock, t.n * (kGated ? kBlock : kTileN), 0, t.expert,
-                            &bar.full[stage]);
-                }
-                __syncwarp();
-                if (lane < pieces) {
-                    if (kGather) load_rows4(a + lane * 4 * kBlock, &amap, kb * kBlock, y, &bar.full[stage]);
-                    else load_2d(a + lane * 32 * kBlock, &amap, kb * kBlock, static_cast<int>(t.first) + lane * 32, &bar.full[stage]);
-                }
-                __syncwarp();
+            // let what is in flight land: every stage that was filled is emptied by the multiplier
+            for (int i = 0; i < kStages; ++i) {
+                if (!wait_for(&bar.empty[stage], phase ^ 1u, &s_stop)) break;
                 if (++stage == kStages) stage = 0, phase ^= 1u;
             }
-        }
-        // let what is in flight land: every stage that was filled is emptied by the multiplier
-        for (int i = 0; i < kStages; ++i) {
-            if (!wait_for(&bar.empty[stage], phase ^ 1u, &s_stop)) break;
-            if (++stage == kStages) stage = 0, phase ^= 1u;
-        }
-    } else if (warp == 1) {
-        // ---- products: one block of 128 columns into one of two accumulators
-        int stage = 0, buf = 0;
-        uint32_t phase = 0, tphase = 0;
-        for (int id = blockIdx.x; tile_of(p, start, ntiles, id, t); id += gridDim.x) {
-            for (int kb = 0; kb < p.kb; ++kb) {
-                if (!wait_for(&bar.tempty[buf], tphase ^ 1u, &s_stop)) goto done;
-                if (!wait_for(&bar.full[stage], phase, &s_stop)) goto done;
-                fence_after();
-                if (elected()) {
-                    const uint64_t a = operand(stages + stage * kStageBytes);
-                    const uint64_t b = operand(stages + stage * kStageBytes + kABytes);
+        } else if (warp == 1) {
+            // ---- products: one block of 128 columns into one of two accumulators
+            int buf = 0;
+            uint32_t tphase = 0;
+            for (int id = blockIdx.x; tile_of(p, start, ntiles, id, t); id += gridDim.x) {
+                for (int kb = 0; kb < p.kb; ++kb) {
+                    if (!wait_for(&bar.tempty[buf], tphase ^ 1u, &s_stop)) goto done;
+                    if (!wait_for(&bar.full[stage], phase, &s_stop)) goto done;
+                    fence_after();
+                    if (elected()) {
+                        const uint64_t a = operand(stages + stage * kStageBytes);
+                        const uint64_t b = operand(stages + stage * kStageBytes + kABytes);
 #pragma unroll
-                    for (int k = 0; k < kBlock / 32; ++k)       // 32 columns an instruction: 2 units of 16 bytes
-                        multiply(tmem + buf * kTileN, a + 2 * k, b + 2 * k, k > 0);
-                    commit(&bar.empty[stage]);
-                    commit(&bar.tfull[buf]);
+                        for (int k = 0; k < kBlock / 32; ++k)       // 32 columns an instruction: 2 units of 16 bytes
+                            multiply(tmem + buf * kTileN, a + 2 * k, b + 2 * k, k > 0);
+                        commit(&bar.empty[stage]);
+                        commit(&bar.tfull[buf]);
+                    }
+                    __syncwarp();
+                    if (++stage == kStages) stage = 0, phase ^= 1u;
+                    buf ^= 1;
+                    if (buf == 0) tphase ^= 1u;
                 }
-                __syncwarp();
-                if (++stage == kStages) stage = 0, phase ^= 1u;
-                buf ^= 1;
-                if (buf == 0) tphase ^= 1u;
+            }
+        } else if (kGather) {
+            // ---- places' rows from anywhere: eight threads a row of 128 bytes, 16 rows a thread.
+            // A stage is handed over kGatherLag blocks later, when its copies are complete.
+            const int i = tid - 64, sub = i >> 3, seg = i & 7;
+            const uint8_t *base = p.a_rows > 0 ? p.values : p.w;
+            int lagging = 0, late = 0;       // stages not yet handed over, the first of them
+            for (int id = blockIdx.x; tile_of(p, start, ntiles, id, t); id += gridDim.x) {
+                int src[16];
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    src[j] = sub + 8 * j < t.here ? p.rows[t.first + sub + 8 * j] : -1;
+                    if (src[j] >= p.a_rows) src[j] = -1;
+                }
+                const int steps = (t.here + 7) / 8;
+                for (int kb = 0; kb < p.kb; ++kb) {
+                    if (!wait_for(&bar.empty[stage], phase ^ 1u, &s_stop)) goto done;
+                    const uint32_t to = smem_u32(stages + stage * kStageBytes) + sub * 128 + ((seg ^ sub) << 4);
+                    const int col = kb * kBlock + seg * 16;
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        if (j < steps) {
+                            const bool there = src[j] >= 0 && col < p.width;
+                            fetch16(to + j * 1024, there ? base + src[j] * p.value_stride + col : base, there);
+                        }
+                    asm volatile("cp.async.commit_group;" ::: "memory");
+                    if (lagging == kGatherLag) {
+                        asm volatile("cp.async.wait_group %0;" ::"n"(kGatherLag) : "memory");
+                        fence_proxy_async_shared();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&bar.full[late]);
+                        if (++late == kStages) late = 0;
+                    } else {
+                        ++lagging;
+                    }
+                    if (++stage == kStages) stage = 0, phase ^= 1u;
+                }
+            }
+            asm volatile("cp.async.wait_group 0;" ::: "memory");
+            fence_proxy_async_shared();
+            __syncwarp();
+            for (; lagging > 0; --lagging) {
+                if (lane == 0) mbar_arrive(&bar.full[late]);
+                if (++late == kStages) late = 0;
             }
         }
     } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kManyRegs));
         // ---- sums: accumulator times the two scales, added up in registers.
         // A warp reads the 32 rows that its number allows, and half the columns:
         // one block of 128, or 64 of the gate's and the same 64 of the up matrix's.
-        const int quad = warp & 3, half = (warp - 2) >> 2, row = quad * 32 + lane;
+        const int quad = warp & 3, half = (warp - 4) >> 2, row = quad * 32 + lane;
         int buf = 0, turn = 0;
         uint32_t tphase = 0;
-        for (int id = blockIdx.x; tile_of(p, start, ntiles, id, t); id += gridDim.x) {
-            const int block = kGated ? t.n : t.n * 2 + half;
-            const bool active = quad * 32 < t.here && block < p.nb;
-            const bool mine = row < t.here;
-            int64_t src = -1;
-            if (mine) {
-                src = kGather ? p.rows[t.first + row] : t.first + row;
-                if (src < 0 || src >= p.a_rows) {
-                    src = -1;
+        // The scales come a group ahead: four blocks' of the thread's row, and
+        // the matrix's of 32 blocks, one to a lane.
+        struct Source {
+            Tile t;
+            bool more, active;
+            int64_t src;               // the thread's row; -1: none
+            const float *a, *w;
+        };
+        auto source = [&](int id) {
+            Source s;
+            s.more = tile_of(p, start, ntiles, id, s.t);
+            if (!s.more) s.t.here = 0, s.t.n = 0, s.t.expert = 0, s.t.first = 0;
+            const int block = kGated ? s.t.n : s.t.n * 2 + half;
+            s.active = quad * 32 < s.t.here && block < p.nb;
+            s.src = -1;
+            if (row < s.t.here) {
+                s.src = kGather ? p.rows[s.t.first + row] : s.t.first + row;
+                if (s.src < 0 || s.src >= p.a_rows) {
+                    s.src = -1;
                     if (p.status) set_error(p.status, EP_ERR_INVALID_ARG);
                 }
             }
-            const float *sa = p.scales + (src < 0 ? 0 : src * p.scale_stride);
-            const float *sw = p.w_scales + (static_cast<int64_t>(t.expert) * (kGated ? 2 : 1) * p.nb + (active ? block : 0)) * p.kb;
-            float acc[128];
+            s.a = p.scales + (s.src < 0 ? 0 : s.src * p.scale_stride);
+            s.w = p.w_scales + (static_cast<int64_t>(s.t.expert) * (kGated ? 2 : 1) * p.nb + (s.active ? block : 0)) * p.kb;
+            return s;
+        };
+        auto row_scales = [&](const Source &s, int kb, float (&x)[4]) {
+            x[0] = x[1] = x[2] = x[3] = 0.0f;
+            if (s.src >= 0 && s.active) {
+                if (p.wide_scales && kb + 4 <= p.kb) {
+                    const float4 v = *reinterpret_cast<const float4 *>(s.a + kb);
+                    x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+                } else {
 #pragma unroll
-            for (int i = 0; i < 128; ++i) acc[i] = 0.0f;
-            for (int kb = 0; kb < p.kb; ++kb) {
-                const float x = src < 0 ? 0.0f : sa[kb];
-                const float s0 = x * sw[kb], s1 = kGated ? x * sw[static_cast<int64_t>(p.nb) * p.kb + kb] : s0;
-                if (!wait_for(&bar.tfull[buf], tphase, &s_stop)) goto done;
-                fence_after();
-                if (active) {
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        float v[32];
-                        const int col = kGated ? (c >> 1) * 128 + half * 64 + (c & 1) * 32 : half * 128 + c * 32;
-                        read32(tmem + (static_cast<uint32_t>(quad * 32) << 16) + buf * kTileN + col, v);
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) acc[c * 32 + i] = fmaf(v[i], c < 2 ? s0 : s1, acc[c * 32 + i]);
-                    }
+                    for (int i = 0; i < 4; ++i)
+                        if (kb + i < p.kb) x[i] = s.a[kb + i];
                 }
-                fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bar.tempty[buf]);
-                buf ^= 1;
-                if (buf == 0) tphase ^= 1u;
             }
+        };
+        const int64_t up = static_cast<int64_t>(p.nb) * p.kb;       // from a gate's scales to the up matrix's
+        auto matrix_scales = [&](const Source &s, int kb, float &w0, float &w1) {
+            const bool ok = s.active && kb + lane < p.kb;
+            w0 = ok ? s.w[kb + lane] : 0.0f;
+            if (kGated) w1 = ok ? s.w[up + kb + lane] : 0.0f;
+        };
+        Source cur = source(blockIdx.x);
+        float xn[4], w0n = 0.0f, w1n = 0.0f;
+        row_scales(cur, 0, xn);
+        matrix_scales(cur, 0, w0n, w1n);
+        for (int id = blockIdx.x; cur.more; id += gridDim.x) {
+            Source next = source(id + gridDim.x);
+            const Tile &t = cur.t;
+            unsigned long long acc[64];
+#pragma unroll
+            for (int i = 0; i < 64; ++i) acc[i] = 0ull;
+            float w0 = 0.0f, w1 = 0.0f;
+            for (int k0 = 0; k0 < p.kb; k0 += 4) {
+                float x[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) x[i] = xn[i];
+                const bool last = k0 + 4 >= p.kb;
+                row_scales(last ? next : cur, last ? 0 : k0 + 4, xn);
+                if ((k0 & 31) == 0) w0 = w0n, w1 = w1n;
+                if ((k0 & 31) == 0 || last) {
+                    // the next 32, or the next tile's first
+                    const bool turn_over = last || k0 + 32 >= p.kb;
+                    matrix_scales(turn_over ? next : cur, turn_over ? 0 : k0 + 32, w0n, w1n);
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if (k0 + i >= p.kb) break;
+                    const float s0 = x[i] * __shfl_sync(0xffffffffu, w0, (k0 + i) & 31);
+                    const float s1 = kGated ? x[i] * __shfl_sync(0xffffffffu, w1, (k0 + i) & 31) : s0;
+                    if (!wait_for(&bar.tfull[buf], tphase, &s_stop)) goto done;
+                    fence_after();
+                    if (cur.active) {
+                        const uint32_t at = tmem + (static_cast<uint32_t>(quad * 32) << 16) + buf * kTileN +
+                                            (kGated ? half * 64 : half * 128);
+                        uint32_t v[2][16];
+                        read16(at, v[0]);
+#pragma unroll
+                        for (int c = 0; c < 8; ++c) {
+                            landed(v[c & 1]);
+                            if (c < 7) read16(at + (kGated && c >= 3 ? 128 + (c - 3) * 16 : (c + 1) * 16), v[(c + 1) & 1]);
+#pragma unroll
+                            for (int q = 0; q < 8; ++q)
+                                add_pair(acc[c * 8 + q], v[c & 1][2 * q], v[c & 1][2 * q + 1], c < 4 ? s0 : s1);
+                        }
+                    }
+                    fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bar.tempty[buf]);
+                    buf ^= 1;
+                    if (buf == 0) tphase ^= 1u;
+                }
+            }
+            const bool mine = row < t.here;
             if (kGated) {
-                float most = kFloor;
+                float y[64], most = kFloor;
 #pragma unroll
                 for (int i = 0; i < 64; ++i) {
-                    const float g = acc[i];
+                    const float g = i & 1 ? high_of(acc[i >> 1]) : low_of(acc[i >> 1]);
+                    const float u = i & 1 ? high_of(acc[32 + (i >> 1)]) : low_of(acc[32 + (i >> 1)]);
                     const int col = t.n * kBlock + half * 64 + i;
-                    acc[i] = src >= 0 && col < p.n ? g / (1.0f + expf(-g)) * acc[64 + i] : 0.0f;
-                    most = max_nan(most, fabsf(acc[i]));
+                    y[i] = cur.src >= 0 && col < p.n ? __fdividef(g, 1.0f + __expf(-g)) * u : 0.0f;
+                    most = max_nan(most, fabsf(y[i]));
                 }
                 // the other half's maximum; two turns, as a warp may be a tile ahead when the other one reads
                 s_most[turn][half][row] = most;
@@ -357,7 +466,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         uint32_t v[8];
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
-                            const float *f = acc + c * 32 + i * 4;
+                            const float *f = y + c * 32 + i * 4;
                             v[i] = pack_fp8x4(f[0] * inv, f[1] * inv, f[2] * inv, f[3] * inv);
                         }
                         if (left >= c * 32 + 32) {
@@ -370,7 +479,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     }
                 }
-            } else if (mine && active) {
+            } else if (mine && cur.active) {
+                const int block = t.n * 2 + half;
                 __nv_bfloat16 *to = p.out + (t.first + row) * p.out_stride + block * kBlock;
                 const int left = p.n - block * kBlock;
 #pragma unroll
@@ -378,7 +488,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     uint32_t v[8];
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
-                        v[i] = src < 0 ? 0u : pack2(acc[c * 16 + 2 * i], acc[c * 16 + 2 * i + 1]);
+                        v[i] = cur.src < 0 ? 0u : pack2(low_of(acc[c * 8 + i]), high_of(acc[c * 8 + i]));
                     if (left >= c * 16 + 16) {
                         store32(to + c * 16, v, p.wide_out);
                     } else if (left >= c * 16 + 8) {
@@ -386,6 +496,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
             }
+            cur = next;
         }
     }
 done:
@@ -437,7 +548,7 @@ ep_status launch_product(const ProductParams &p, int device, cudaStream_t st) {
     // without rows to read (every place's row is then out of range) any readable row will do
     const cuuint64_t adims[2] = {static_cast<cuuint64_t>(p.width), static_cast<cuuint64_t>(p.a_rows ? p.a_rows : 1)};
     const cuuint64_t astride[1] = {static_cast<cuuint64_t>(p.a_rows ? p.value_stride : p.width)};
-    const cuuint32_t abox[2] = {kBlock, kGather ? 1u : 32u};
+    const cuuint32_t abox[2] = {kBlock, 32u};
     const cuuint64_t wdims[4] = {static_cast<cuuint64_t>(p.width), static_cast<cuuint64_t>(p.n), kGated ? 2u : 1u,
                                  static_cast<cuuint64_t>(p.experts)};
     const cuuint64_t matrix = static_cast<cuuint64_t>(p.width) * p.n;
@@ -503,6 +614,7 @@ extern "C" ep_status ep_expert_product(int64_t places, int64_t a_rows, int32_t e
     p.out_scales = out_scales, p.out_scale_stride = out_scale_stride;
     p.status = status;
     p.experts = experts, p.width = width, p.n = out, p.nb = nb, p.kb = kb;
+    p.wide_scales = aligned(scales, 16) && scale_stride % 4 == 0;
     p.wide_out = gated ? aligned(out_values, 32) && out_value_stride % 32 == 0
                        : aligned(out_bf16, 32) && out_stride % 16 == 0;
     // tiles are counted in 32 bits
