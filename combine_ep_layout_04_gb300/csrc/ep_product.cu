@@ -35,32 +35,44 @@ __device__ __forceinline__ bool bad_segment(const ProductParams &p, int e) {
 }
 
 // ------------------------------------------------------------------ tile sizes
-constexpr int kTileM = 128;            // places of a tile
+// Two CTAs of a cluster share a tile: each holds its 128 places' rows, its
+// half of the matrix rows, and the sums of its places over all the tile's
+// columns; the products read both halves.
+constexpr int kRows = 128;             // places of a CTA
+constexpr int kTileM = 2 * kRows;      // places of a tile
 constexpr int kTileN = 256;            // matrix rows of a tile: 256 columns, or 128 of each matrix of a gated pair
-constexpr int kStages = 4;             // blocks of 128 columns in flight
-constexpr int kABytes = kTileM * kBlock, kBBytes = kTileN * kBlock, kStageBytes = kABytes + kBBytes;
+constexpr int kStages = 6;             // blocks of 128 columns in flight
+constexpr int kHalfN = kTileN / 2;     // columns of an accumulator: four of them, so that the products run two blocks ahead
+constexpr int kABytes = kRows * kBlock, kBBytes = kTileN / 2 * kBlock, kStageBytes = kABytes + kBBytes;
 constexpr int kSums = 8;               // warps that hold the sums: two warpgroups
 constexpr int kGatherWarps = 2;        // warps that fetch rows one by one
-constexpr int kGatherLag = 2;          // blocks of 128 columns a gathering thread has in flight
+constexpr int kGatherLag = 3;          // blocks of 128 columns a gathering thread has in flight
 constexpr int kThreads = 32 * (4 + kSums);
+// Scales of the blocks under way, by step.  A slot is written again 16 steps
+// later, when the stage of 10 steps later has been multiplied, which took the
+// accumulators of 8 steps later: its sums are done by then.
+constexpr int kSlots = 16;
+static_assert(kSlots - kStages - 2 > 0, "a slot would be written before it is read");
 // Registers: a sums thread holds 128 fp32 sums; the first warpgroup gives up
 // what it does not need (the two shares are the launch's 168 a thread).
-constexpr int kFewRegs = 72, kManyRegs = 216;
+constexpr int kFewRegs = 120, kManyRegs = 192;
 static_assert(128 * kFewRegs + 256 * kManyRegs <= kThreads * 168, "register shares exceed the launch's");
 
+// The first CTA's are used for full and tempty, each CTA's own for the others.
 struct Barriers {
-    uint64_t full[kStages], empty[kStages];      // a stage has landed / has been multiplied
-    uint64_t tfull[2], tempty[2];                // an accumulator is complete / has been read
+    uint64_t full[kStages], empty[kStages];      // a stage has landed in both CTAs / has been multiplied
+    uint64_t tfull[4], tempty[4];                // an accumulator is complete / has been read by both CTAs
     uint64_t pair[4];                            // both halves of 32 rows have their maxima
 };
 
 struct Tile {
-    int expert, m0, here, n;       // first place within the expert, places of the tile, column tile
-    int64_t first;                 // its first place
+    int expert, here, n;       // places of this CTA, column tile
+    int first;                 // this CTA's first place
+    bool any;                  // the tile exists
 };
 
-// Wait of a whole warp with a limit; the first one to run out ends the others'
-// waits.  The answer is the same for every lane.
+// Waits of a whole warp with a limit, on barriers that either CTA arrives at;
+// the first one to run out ends the others'.  The answer is the same for every lane.
 __device__ __forceinline__ bool wait_for(uint64_t *bar, uint32_t parity, volatile int *stop) {
     if (__all_sync(0xffffffffu, mbar_try(bar, parity))) return true;
     const uint64_t t0 = globaltimer_ns();
@@ -73,19 +85,42 @@ __device__ __forceinline__ bool wait_for(uint64_t *bar, uint32_t parity, volatil
     return true;
 }
 
-// ---- tensor maps, tensor cores and their memory (PTX)
-__device__ __forceinline__ void load_4d(void *dst, const CUtensorMap *map, int x, int y, int z, int w, uint64_t *bar) {
+// ---- clusters, tensor maps, tensor cores and their memory (PTX)
+__device__ __forceinline__ uint32_t cta_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// the first CTA's copy of a barrier
+__device__ __forceinline__ uint32_t first_cta(uint64_t *bar) {
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(a) : "r"(smem_u32(bar)));
+    return a;
+}
+// Arrives at a barrier of either CTA.  What this hands over is shared or tensor
+// memory of the arriving thread's own SM, complete there before it arrives, so
+// the order within the SM is enough; a release at cluster scope waits for the
+// thread's global accesses too and doubled the time of a step (0.57 -> 1.16 us).
+__device__ __forceinline__ void arrive_cluster(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void load_4d(void *dst, const CUtensorMap *map, int x, int y, int z, int w, uint32_t bar) {
     asm volatile(
-        "cp.async.bulk.tensor.4d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(
+        "cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(
             smem_u32(dst)),
-        "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
+        "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
         : "memory");
 }
-__device__ __forceinline__ void load_2d(void *dst, const CUtensorMap *map, int x, int y, uint64_t *bar) {
+__device__ __forceinline__ void load_2d(void *dst, const CUtensorMap *map, int x, int y, uint32_t bar) {
     asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3}], [%4];" ::"r"(
             smem_u32(dst)),
-        "l"(map), "r"(x), "r"(y), "r"(smem_u32(bar))
+        "l"(map), "r"(x), "r"(y), "r"(bar)
         : "memory");
 }
 // 16 bytes, or zeros without a source
@@ -102,43 +137,43 @@ __device__ __forceinline__ bool elected() {
 __device__ __forceinline__ uint64_t operand(const void *p) {
     return (static_cast<uint64_t>(smem_u32(p)) >> 4) | (1ull << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
 }
-// e4m3 x e4m3 -> fp32, both operands with dense columns, kTileM x kTileN.
-constexpr uint32_t kShape = (1u << 4) | (static_cast<uint32_t>(kTileN >> 3) << 17) | (static_cast<uint32_t>(kTileM >> 4) << 24);
+// e4m3 x e4m3 -> fp32, both operands with dense columns, kTileM x kHalfN.
+constexpr uint32_t kShape = (1u << 4) | (static_cast<uint32_t>(kHalfN >> 3) << 17) | (static_cast<uint32_t>(kTileM >> 4) << 24);
 
 __device__ __forceinline__ void multiply(uint32_t acc, uint64_t a, uint64_t b, bool add) {
     asm volatile(
         "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(acc),
+        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(acc),
         "l"(a), "l"(b), "r"(kShape), "r"(static_cast<uint32_t>(add))
         : "memory");
 }
+// arrives at both CTAs' copies once the products so far are done
 __device__ __forceinline__ void commit(uint64_t *bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
-                 : "memory");
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(smem_u32(bar)),
+        "h"(static_cast<uint16_t>(3))
+        : "memory");
 }
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-// 16 columns of the thread's row of an accumulator, as pairs; complete after
-// landed(), which the pairs pass through so that no use moves before it.
-__device__ __forceinline__ void read16(uint32_t at, uint32_t (&r)[16]) {
+// 32 columns of the thread's row of an accumulator
+__device__ __forceinline__ void read32(uint32_t at, uint32_t (&r)[32]) {
     asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, "
+        "%23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]),
+          "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]),
+          "=r"(r[30]), "=r"(r[31])
         : "r"(at)
         : "memory");
 }
-__device__ __forceinline__ void landed(uint32_t (&r)[16]) {
-    asm volatile("tcgen05.wait::ld.sync.aligned;"
-                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
-                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
-                 :
-                 : "memory");
-}
 // sums of two neighbouring columns: acc += v * s
 __device__ __forceinline__ void add_pair(unsigned long long &acc, uint32_t v0, uint32_t v1, float s) {
-    asm("{\n\t.reg .b64 v, s;\n\tmov.b64 v, {%1, %2};\n\tmov.b64 s, {%3, %3};\n\tfma.rn.f32x2 %0, v, s, %0;\n\t}"
+    asm volatile("{\n\t.reg .b64 v, s;\n\tmov.b64 v, {%1, %2};\n\tmov.b64 s, {%3, %3};\n\tfma.rn.f32x2 %0, v, s, %0;\n\t}"
         : "+l"(acc)
         : "r"(v0), "r"(v1), "r"(__float_as_uint(s)));
 }
@@ -159,10 +194,11 @@ __device__ __forceinline__ void store32(void *to, const uint32_t (&v)[8], bool w
 }
 
 // Tiles in the order expert, column tile, place tile (place tiles next to each
-// other, so that CTAs that run together share a matrix tile and an expert's
-// rows in L2).  start[e] = tiles before expert e, start[experts] = all.
-__device__ __forceinline__ bool tile_of(const ProductParams &p, const int *start, int ntiles, int id, Tile &t) {
-    if (id >= start[p.experts]) return false;
+// other, so that clusters that run together share a matrix tile and an
+// expert's rows in L2).  start[e] = tiles before expert e, start[experts] = all.
+__device__ __forceinline__ Tile tile_of(const ProductParams &p, const int *start, int rank, int id) {
+    Tile t{};
+    if (id >= start[p.experts]) return t;
     int lo = 0, hi = p.experts;
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
@@ -170,39 +206,42 @@ __device__ __forceinline__ bool tile_of(const ProductParams &p, const int *start
         else hi = mid;
     }
     const int count = count_of(p, lo), mtiles = (count + kTileM - 1) / kTileM, at = id - start[lo];
+    t.any = true;
     t.expert = lo;
     t.n = at / mtiles;
-    t.m0 = (at - t.n * mtiles) * kTileM;
-    t.here = min(kTileM, count - t.m0);
-    t.first = p.expert_off[lo] + static_cast<int64_t>(t.m0);
-    return true;
+    const int m0 = (at - t.n * mtiles) * kTileM + rank * kRows;
+    t.here = max(0, min(kRows, count - m0));
+    t.first = p.expert_off[lo] + m0;
+    return t;
 }
 
 template <bool kGated, bool kGather>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     product_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap wmap,
                    const __grid_constant__ ProductParams p) {
     extern __shared__ uint8_t smem_raw[];
     __shared__ Barriers bar;
     __shared__ uint32_t s_tmem;
     __shared__ int s_stop, s_scan[kThreads / 32];
-    __shared__ float s_most[2][2][kTileM];      // by turn, half, row
+    __shared__ float s_most[2][2][kRows];      // by turn, half, row
+    __shared__ float s_x[kSlots][kRows], s_w[kSlots][2];      // scales of the rows, of the matrix blocks
     uint8_t *stages = smem_raw + (-smem_u32(smem_raw) & 1023u);
     int *start = reinterpret_cast<int *>(stages + kStages * kStageBytes);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int rank = static_cast<int>(cta_rank()), cluster = blockIdx.x >> 1, clusters = gridDim.x >> 1;
     const int ntiles = (p.n + (kGated ? kBlock : kTileN) - 1) / (kGated ? kBlock : kTileN);
 
     if (tid == 0) {
         for (int i = 0; i < kStages; ++i)
-            mbar_init(&bar.full[i], kGather ? 1 + kGatherWarps : 1), mbar_init(&bar.empty[i], 1);
-        for (int i = 0; i < 2; ++i) mbar_init(&bar.tfull[i], 1), mbar_init(&bar.tempty[i], kSums);
+            mbar_init(&bar.full[i], 2 + (kGather ? 2 * kGatherWarps : 0)), mbar_init(&bar.empty[i], 1);
+        for (int i = 0; i < 4; ++i) mbar_init(&bar.tfull[i], 1), mbar_init(&bar.tempty[i], kSums);
         for (int i = 0; i < 4; ++i) mbar_init(&bar.pair[i], 2);
         mbar_fence_init();
         s_stop = 0;
     }
     if (warp == 1) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&s_tmem)) : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&s_tmem)) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
     }
     // tiles before each expert
     int carry = 0;
@@ -233,31 +272,98 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (tid == 0) start[p.experts] = carry;
     fence_before();
     __syncthreads();
+    cluster_sync();
     fence_after();
     const uint32_t tmem = s_tmem;
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFewRegs));
-        Tile t;
         int stage = 0;
         uint32_t phase = 0;
         if (warp == 0) {
-            // ---- loads: matrix rows, and places' rows where they lie in order, 128 columns at a time
-            for (int id = blockIdx.x; tile_of(p, start, ntiles, id, t); id += gridDim.x) {
+            // ---- loads: this CTA's matrix rows, its places' rows where they lie in order, and the
+            // scales, which come four blocks ahead: of four rows a lane, and of the tile's two
+            // matrix blocks, one block of 128 columns to each of eight lanes.
+            int slot = 0;
+            for (int id = cluster;; id += clusters) {
+                const Tile t = tile_of(p, start, rank, id);
+                if (!t.any) break;
                 const int pieces = kGather ? 0 : (t.here + 31) / 32;
-                for (int kb = 0; kb < p.kb; ++kb) {
-                    if (!wait_for(&bar.empty[stage], phase ^ 1u, &s_stop)) goto done;
-                    uint8_t *a = stages + stage * kStageBytes;
-                    if (lane == 0) {
-                        mbar_arrive_expect_tx(&bar.full[stage], kBBytes + pieces * 32 * kBlock);
-                        load_4d(a + kABytes, &wmap, kb * kBlock, t.n * (kGated ? kBlock : kTileN), 0, t.expert,
-                                &bar.full[stage]);
+                // what both CTAs load: the other one's places too, in whole pieces
+                const int there = kGather ? 0 : (tile_of(p, start, rank ^ 1, id).here + 31) / 32;
+                const float *sa[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int row = j * 32 + lane;
+                    sa[j] = nullptr;
+                    if (row < t.here) {
+                        const int src = kGather ? p.rows[t.first + row] : t.first + row;
+                        if (src >= 0 && src < p.a_rows) sa[j] = p.scales + src * p.scale_stride;
+                        else if (p.status) set_error(p.status, EP_ERR_INVALID_ARG);
                     }
-                    __syncwarp();
-                    if (!kGather && lane < pieces)
-                        load_2d(a + lane * 32 * kBlock, &amap, kb * kBlock, static_cast<int>(t.first) + lane * 32,
-                                &bar.full[stage]);
-                    __syncwarp();
-                    if (++stage == kStages) stage = 0, phase ^= 1u;
+                }
+                const int block = kGated ? t.n : t.n * 2 + ((lane >> 2) & 1);
+                const float *sw = p.w_scales + (lane & 3) +
+                                  ((static_cast<int64_t>(t.expert) * (kGated ? 2 : 1) + (kGated ? (lane >> 2) & 1 : 0)) * p.nb +
+                                   min(block, p.nb - 1)) * p.kb;
+                float x[4][4], w = 0.0f;
+                auto scales = [&](int kb) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        x[j][0] = x[j][1] = x[j][2] = x[j][3] = 0.0f;
+                        if (!sa[j]) continue;
+                        if (p.wide_scales && kb + 4 <= p.kb) {
+                            const float4 v = *reinterpret_cast<const float4 *>(sa[j] + kb);
+                            x[j][0] = v.x, x[j][1] = v.y, x[j][2] = v.z, x[j][3] = v.w;
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                if (kb + i < p.kb) x[j][i] = sa[j][kb + i];
+                        }
+                    }
+                    if (lane < 8 && kb + (lane & 3) < p.kb) w = sw[kb];
+                };
+                scales(0);
+                for (int k0 = 0; k0 < p.kb; k0 += 4) {
+                    float xs[4][4];
+                    const float ws = w;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) xs[j][i] = x[j][i];
+                    scales(k0 + 4);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int kb = k0 + i;
+                        if (kb >= p.kb) break;
+                        if (!wait_for(&bar.empty[stage], phase ^ 1u, &s_stop)) goto done;
+                        uint8_t *a = stages + stage * kStageBytes;
+                        const uint32_t full = first_cta(&bar.full[stage]);
+                        if (lane == 0) {
+                            // 64 matrix rows for each accumulator: the gate's here and the up matrix's
+                            // there, or the two halves of a block of 128
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                const int n = kGated ? t.n * kBlock + h * 64 : t.n * kTileN + h * kHalfN + rank * 64;
+                                load_4d(a + kABytes + h * 64 * kBlock, &wmap, kb * kBlock, n, kGated ? rank : 0, t.expert,
+                                        full);
+                            }
+                        }
+                        __syncwarp();
+                        if (!kGather && lane < pieces)
+                            load_2d(a + lane * 32 * kBlock, &amap, kb * kBlock, t.first + lane * 32, full);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) s_x[slot][j * 32 + lane] = xs[j][i];
+                        if (lane < 8 && (lane & 3) == i) s_w[slot][lane >> 2] = ws;
+                        __syncwarp();
+                        if (lane == 0) {
+                            if (rank == 0)
+                                mbar_arrive_expect_tx(&bar.full[stage], 2 * kBBytes + (pieces + there) * 32 * kBlock);
+                            else
+                                arrive_cluster(full);
+                        }
+                        slot = (slot + 1) % kSlots;
+                        if (++stage == kStages) stage = 0, phase ^= 1u;
+                    }
                 }
             }
             // let what is in flight land: every stage that was filled is emptied by the multiplier
@@ -266,27 +372,33 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (++stage == kStages) stage = 0, phase ^= 1u;
             }
         } else if (warp == 1) {
-            // ---- products: one block of 128 columns into one of two accumulators
-            int buf = 0;
+            // ---- products, by the first CTA: a block of 128 columns into an accumulator for each
+            // half of the tile's columns; two turns of them
+            int turn = 0;
             uint32_t tphase = 0;
-            for (int id = blockIdx.x; tile_of(p, start, ntiles, id, t); id += gridDim.x) {
+            const int total = rank == 0 ? start[p.experts] : 0;
+            for (int id = cluster; id < total; id += clusters) {
                 for (int kb = 0; kb < p.kb; ++kb) {
-                    if (!wait_for(&bar.tempty[buf], tphase ^ 1u, &s_stop)) goto done;
                     if (!wait_for(&bar.full[stage], phase, &s_stop)) goto done;
-                    fence_after();
-                    if (elected()) {
-                        const uint64_t a = operand(stages + stage * kStageBytes);
-                        const uint64_t b = operand(stages + stage * kStageBytes + kABytes);
 #pragma unroll
-                        for (int k = 0; k < kBlock / 32; ++k)       // 32 columns an instruction: 2 units of 16 bytes
-                            multiply(tmem + buf * kTileN, a + 2 * k, b + 2 * k, k > 0);
-                        commit(&bar.empty[stage]);
-                        commit(&bar.tfull[buf]);
+                    for (int h = 0; h < 2; ++h) {
+                        const int buf = turn * 2 + h;
+                        if (!wait_for(&bar.tempty[buf], tphase ^ 1u, &s_stop)) goto done;
+                        fence_after();
+                        if (elected()) {
+                            const uint64_t a = operand(stages + stage * kStageBytes);
+                            const uint64_t b = operand(stages + stage * kStageBytes + kABytes + h * 64 * kBlock);
+#pragma unroll
+                            for (int k = 0; k < kBlock / 32; ++k)       // 32 columns an instruction: 2 units of 16 bytes
+                                multiply(tmem + buf * kHalfN, a + 2 * k, b + 2 * k, k > 0);
+                            commit(&bar.tfull[buf]);
+                            if (h == 1) commit(&bar.empty[stage]);
+                        }
+                        __syncwarp();
                     }
-                    __syncwarp();
                     if (++stage == kStages) stage = 0, phase ^= 1u;
-                    buf ^= 1;
-                    if (buf == 0) tphase ^= 1u;
+                    turn ^= 1;
+                    if (turn == 0) tphase ^= 1u;
                 }
             }
         } else if (kGather) {
@@ -295,7 +407,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int i = tid - 64, sub = i >> 3, seg = i & 7;
             const uint8_t *base = p.a_rows > 0 ? p.values : p.w;
             int lagging = 0, late = 0;       // stages not yet handed over, the first of them
-            for (int id = blockIdx.x; tile_of(p, start, ntiles, id, t); id += gridDim.x) {
+            for (int id = cluster;; id += clusters) {
+                const Tile t = tile_of(p, start, rank, id);
+                if (!t.any) break;
                 int src[16];
 #pragma unroll
                 for (int j = 0; j < 16; ++j) {
@@ -318,7 +432,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         asm volatile("cp.async.wait_group %0;" ::"n"(kGatherLag) : "memory");
                         fence_proxy_async_shared();
                         __syncwarp();
-                        if (lane == 0) mbar_arrive(&bar.full[late]);
+                        if (lane == 0) arrive_cluster(first_cta(&bar.full[late]));
                         if (++late == kStages) late = 0;
                     } else {
                         ++lagging;
@@ -330,123 +444,58 @@ __global__ void __launch_bounds__(kThreads, 1)
             fence_proxy_async_shared();
             __syncwarp();
             for (; lagging > 0; --lagging) {
-                if (lane == 0) mbar_arrive(&bar.full[late]);
+                if (lane == 0) arrive_cluster(first_cta(&bar.full[late]));
                 if (++late == kStages) late = 0;
             }
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kManyRegs));
         // ---- sums: accumulator times the two scales, added up in registers.
-        // A warp reads the 32 rows that its number allows, and half the columns:
-        // one block of 128, or 64 of the gate's and the same 64 of the up matrix's.
+        // A warp reads the 32 rows that its number allows, and one half's
+        // accumulators: a block of 128 columns, or 64 of the gate's and the same 64
+        // of the up matrix's.
         const int quad = warp & 3, half = (warp - 4) >> 2, row = quad * 32 + lane;
-        int buf = 0, turn = 0;
-        uint32_t tphase = 0;
-        // The scales come a group ahead: four blocks' of the thread's row, and
-        // the matrix's of 32 blocks, one to a lane.
-        struct Source {
-            Tile t;
-            bool more, active;
-            int64_t src;               // the thread's row; -1: none
-            const float *a, *w;
-        };
-        auto source = [&](int id) {
-            Source s;
-            s.more = tile_of(p, start, ntiles, id, s.t);
-            if (!s.more) s.t.here = 0, s.t.n = 0, s.t.expert = 0, s.t.first = 0;
-            const int block = kGated ? s.t.n : s.t.n * 2 + half;
-            s.active = quad * 32 < s.t.here && block < p.nb;
-            s.src = -1;
-            if (row < s.t.here) {
-                s.src = kGather ? p.rows[s.t.first + row] : s.t.first + row;
-                if (s.src < 0 || s.src >= p.a_rows) {
-                    s.src = -1;
-                    if (p.status) set_error(p.status, EP_ERR_INVALID_ARG);
-                }
-            }
-            s.a = p.scales + (s.src < 0 ? 0 : s.src * p.scale_stride);
-            s.w = p.w_scales + (static_cast<int64_t>(s.t.expert) * (kGated ? 2 : 1) * p.nb + (s.active ? block : 0)) * p.kb;
-            return s;
-        };
-        auto row_scales = [&](const Source &s, int kb, float (&x)[4]) {
-            x[0] = x[1] = x[2] = x[3] = 0.0f;
-            if (s.src >= 0 && s.active) {
-                if (p.wide_scales && kb + 4 <= p.kb) {
-                    const float4 v = *reinterpret_cast<const float4 *>(s.a + kb);
-                    x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (kb + i < p.kb) x[i] = s.a[kb + i];
-                }
-            }
-        };
-        const int64_t up = static_cast<int64_t>(p.nb) * p.kb;       // from a gate's scales to the up matrix's
-        auto matrix_scales = [&](const Source &s, int kb, float &w0, float &w1) {
-            const bool ok = s.active && kb + lane < p.kb;
-            w0 = ok ? s.w[kb + lane] : 0.0f;
-            if (kGated) w1 = ok ? s.w[up + kb + lane] : 0.0f;
-        };
-        Source cur = source(blockIdx.x);
-        float xn[4], w0n = 0.0f, w1n = 0.0f;
-        row_scales(cur, 0, xn);
-        matrix_scales(cur, 0, w0n, w1n);
-        for (int id = blockIdx.x; cur.more; id += gridDim.x) {
-            Source next = source(id + gridDim.x);
-            const Tile &t = cur.t;
+        int turn = 0;
+        uint32_t step = 0;
+        for (int id = cluster;; id += clusters) {
+            const Tile cur = tile_of(p, start, rank, id);
+            if (!cur.any) break;
+            const bool active = quad * 32 < cur.here && (kGated || cur.n * 2 + half < p.nb);
             unsigned long long acc[64];
 #pragma unroll
             for (int i = 0; i < 64; ++i) acc[i] = 0ull;
-            float w0 = 0.0f, w1 = 0.0f;
-            for (int k0 = 0; k0 < p.kb; k0 += 4) {
-                float x[4];
+#pragma unroll 1
+            for (int kb = 0; kb < p.kb; ++kb, ++step) {
+                const int buf = half + 2 * (step & 1);       // this warp's accumulators: half, and half + 2
+                if (!wait_for(&bar.tfull[buf], (step >> 1) & 1, &s_stop)) goto done;
+                fence_after();
+                if (active) {
+                    const float x = s_x[step % kSlots][row];
+                    const float s0 = x * s_w[step % kSlots][kGated ? 0 : half], s1 = kGated ? x * s_w[step % kSlots][1] : s0;
+                    const uint32_t at = tmem + (static_cast<uint32_t>(quad * 32) << 16) + buf * kHalfN;
+                    uint32_t v[32];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) x[i] = xn[i];
-                const bool last = k0 + 4 >= p.kb;
-                row_scales(last ? next : cur, last ? 0 : k0 + 4, xn);
-                if ((k0 & 31) == 0) w0 = w0n, w1 = w1n;
-                if ((k0 & 31) == 0 || last) {
-                    // the next 32, or the next tile's first
-                    const bool turn_over = last || k0 + 32 >= p.kb;
-                    matrix_scales(turn_over ? next : cur, turn_over ? 0 : k0 + 32, w0n, w1n);
-                }
+                    for (int c = 0; c < 4; ++c) {
+                        read32(at + c * 32, v);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    if (k0 + i >= p.kb) break;
-                    const float s0 = x[i] * __shfl_sync(0xffffffffu, w0, (k0 + i) & 31);
-                    const float s1 = kGated ? x[i] * __shfl_sync(0xffffffffu, w1, (k0 + i) & 31) : s0;
-                    if (!wait_for(&bar.tfull[buf], tphase, &s_stop)) goto done;
-                    fence_after();
-                    if (cur.active) {
-                        const uint32_t at = tmem + (static_cast<uint32_t>(quad * 32) << 16) + buf * kTileN +
-                                            (kGated ? half * 64 : half * 128);
-                        uint32_t v[2][16];
-                        read16(at, v[0]);
-#pragma unroll
-                        for (int c = 0; c < 8; ++c) {
-                            landed(v[c & 1]);
-                            if (c < 7) read16(at + (kGated && c >= 3 ? 128 + (c - 3) * 16 : (c + 1) * 16), v[(c + 1) & 1]);
-#pragma unroll
-                            for (int q = 0; q < 8; ++q)
-                                add_pair(acc[c * 8 + q], v[c & 1][2 * q], v[c & 1][2 * q + 1], c < 4 ? s0 : s1);
-                        }
+                        for (int q = 0; q < 16; ++q)
+                            add_pair(acc[c * 16 + q], v[2 * q], v[2 * q + 1], c < 2 ? s0 : s1);
                     }
-                    fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&bar.tempty[buf]);
-                    buf ^= 1;
-                    if (buf == 0) tphase ^= 1u;
                 }
+                fence_before();
+                __syncwarp();
+                if (lane == 0) arrive_cluster(first_cta(&bar.tempty[buf]));
             }
-            const bool mine = row < t.here;
+            const bool mine = row < cur.here;
+            const int64_t place = cur.first + row;
             if (kGated) {
                 float y[64], most = kFloor;
 #pragma unroll
                 for (int i = 0; i < 64; ++i) {
                     const float g = i & 1 ? high_of(acc[i >> 1]) : low_of(acc[i >> 1]);
                     const float u = i & 1 ? high_of(acc[32 + (i >> 1)]) : low_of(acc[32 + (i >> 1)]);
-                    const int col = t.n * kBlock + half * 64 + i;
-                    y[i] = cur.src >= 0 && col < p.n ? __fdividef(g, 1.0f + __expf(-g)) * u : 0.0f;
+                    const int col = cur.n * kBlock + half * 64 + i;
+                    y[i] = col < p.n ? __fdividef(g, 1.0f + __expf(-g)) * u : 0.0f;
                     most = max_nan(most, fabsf(y[i]));
                 }
                 // the other half's maximum; two turns, as a warp may be a tile ahead when the other one reads
@@ -458,9 +507,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 turn ^= 1;
                 if (mine) {
                     const float inv = kFp8Max / most;
-                    if (half == 0) p.out_scales[(t.first + row) * p.out_scale_stride + t.n] = most * (1.0f / kFp8Max);
-                    uint8_t *to = p.out_values + (t.first + row) * p.out_value_stride + t.n * kBlock + half * 64;
-                    const int left = p.n - (t.n * kBlock + half * 64);
+                    if (half == 0) p.out_scales[place * p.out_scale_stride + cur.n] = most * (1.0f / kFp8Max);
+                    uint8_t *to = p.out_values + place * p.out_value_stride + cur.n * kBlock + half * 64;
+                    const int left = p.n - (cur.n * kBlock + half * 64);
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
                         uint32_t v[8];
@@ -479,16 +528,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     }
                 }
-            } else if (mine && cur.active) {
-                const int block = t.n * 2 + half;
-                __nv_bfloat16 *to = p.out + (t.first + row) * p.out_stride + block * kBlock;
+            } else if (mine && active) {
+                const int block = cur.n * 2 + half;
+                __nv_bfloat16 *to = p.out + place * p.out_stride + block * kBlock;
                 const int left = p.n - block * kBlock;
 #pragma unroll
                 for (int c = 0; c < 8; ++c) {
                     uint32_t v[8];
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
-                        v[i] = cur.src < 0 ? 0u : pack2(low_of(acc[c * 8 + i]), high_of(acc[c * 8 + i]));
+                        v[i] = pack2(low_of(acc[c * 8 + i]), high_of(acc[c * 8 + i]));
                     if (left >= c * 16 + 16) {
                         store32(to + c * 16, v, p.wide_out);
                     } else if (left >= c * 16 + 8) {
@@ -496,7 +545,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
             }
-            cur = next;
         }
     }
 done:
@@ -511,7 +559,9 @@ done:
         }
         __syncthreads();
     }
-    if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+    // the other CTA's products read this one's memory, and its arrivals come here
+    cluster_sync();
+    if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
 }
 
 // ------------------------------------------------------------------ host side
@@ -553,7 +603,7 @@ ep_status launch_product(const ProductParams &p, int device, cudaStream_t st) {
                                  static_cast<cuuint64_t>(p.experts)};
     const cuuint64_t matrix = static_cast<cuuint64_t>(p.width) * p.n;
     const cuuint64_t wstride[3] = {static_cast<cuuint64_t>(p.width), matrix, matrix * (kGated ? 2 : 1)};
-    const cuuint32_t wbox[4] = {kBlock, static_cast<cuuint32_t>(kGated ? kBlock : kTileN), kGated ? 2u : 1u, 1};
+    const cuuint32_t wbox[4] = {kBlock, 64, 1, 1};
     if (!encode(&amap, p.a_rows ? p.values : p.w, 2, adims, astride, abox) || !encode(&wmap, p.w, 4, wdims, wstride, wbox))
         return EP_ERR_CUDA;
     const size_t smem = 1024 + kStages * kStageBytes + sizeof(int) * (p.experts + 1);
@@ -567,7 +617,7 @@ ep_status launch_product(const ProductParams &p, int device, cudaStream_t st) {
     const int64_t ntiles = (p.n + (kGated ? kBlock : kTileN) - 1) / (kGated ? kBlock : kTileN);
     // every expert may leave one tile short
     const int64_t tiles = (p.places / kTileM + (p.places < p.experts ? p.places : p.experts)) * ntiles;
-    const unsigned grid = static_cast<unsigned>(tiles < sms ? tiles : sms);
+    const unsigned grid = 2 * static_cast<unsigned>(tiles < sms / 2 ? tiles : sms / 2);
     product_kernel<kGated, kGather><<<grid, kThreads, smem, st>>>(amap, wmap, p);
     return launched();
 }
