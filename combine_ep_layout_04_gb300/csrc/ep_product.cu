@@ -45,19 +45,23 @@ constexpr int kStages = 6;             // blocks of 128 columns in flight
 constexpr int kHalfN = kTileN / 2;     // columns of an accumulator: four of them, so that the products run two blocks ahead
 constexpr int kABytes = kRows * kBlock, kBBytes = kTileN / 2 * kBlock, kStageBytes = kABytes + kBBytes;
 constexpr int kSums = 8;               // warps that hold the sums: two warpgroups
-constexpr int kGatherWarps = 2;        // warps that fetch rows one by one
+constexpr int kGatherWarps = 4;        // warps that fetch rows one by one, where rows are given: a warpgroup more
+constexpr int kGatherRows = kRows / (kGatherWarps * 4);      // rows a gathering thread has a part of
 constexpr int kGatherLag = 3;          // blocks of 128 columns a gathering thread has in flight
-constexpr int kThreads = 32 * (4 + kSums);
+constexpr int threads_of(bool gather) { return 32 * (4 + kSums + (gather ? kGatherWarps : 0)); }
+// Registers: a sums thread holds 128 fp32 sums; the other warpgroups give up
+// what they do not need.  The shares stay within the launch's.
+constexpr int kLoadRegs = 104, kGatherRegs = 56;
+constexpr int sum_regs(bool gather) { return gather ? 176 : 200; }
+constexpr int launch_regs(bool gather) { return 65536 / threads_of(gather) / 8 * 8; }
+static_assert(128 * kLoadRegs + 256 * sum_regs(false) <= threads_of(false) * launch_regs(false) &&
+              128 * (kLoadRegs + kGatherRegs) + 256 * sum_regs(true) <= threads_of(true) * launch_regs(true),
+              "register shares exceed the launch's");
 // Scales of the blocks under way, by step.  A slot is written again 16 steps
 // later, when the stage of 10 steps later has been multiplied, which took the
 // accumulators of 8 steps later: its sums are done by then.
 constexpr int kSlots = 16;
 static_assert(kSlots - kStages - 2 > 0, "a slot would be written before it is read");
-// Registers: a sums thread holds 128 fp32 sums; the first warpgroup gives up
-// what it does not need (the two shares are the launch's 168 a thread).
-constexpr int kFewRegs = 120, kManyRegs = 192;
-static_assert(128 * kFewRegs + 256 * kManyRegs <= kThreads * 168, "register shares exceed the launch's");
-
 // The first CTA's are used for full and tempty, each CTA's own for the others.
 struct Barriers {
     uint64_t full[kStages], empty[kStages];      // a stage has landed in both CTAs / has been multiplied
@@ -78,6 +82,19 @@ __device__ __forceinline__ bool wait_for(uint64_t *bar, uint32_t parity, volatil
     const uint64_t t0 = globaltimer_ns();
     while (!__all_sync(0xffffffffu, mbar_try(bar, parity))) {
         if (__any_sync(0xffffffffu, *stop != 0 || globaltimer_ns() - t0 > kDefaultTimeoutNs)) {
+            *stop = 1;
+            return false;
+        }
+    }
+    return true;
+}
+
+// The same for one thread.
+__device__ __forceinline__ bool wait_alone(uint64_t *bar, uint32_t parity, volatile int *stop) {
+    if (mbar_try(bar, parity)) return true;
+    const uint64_t t0 = globaltimer_ns();
+    while (!mbar_try(bar, parity)) {
+        if (*stop != 0 || globaltimer_ns() - t0 > kDefaultTimeoutNs) {
             *stop = 1;
             return false;
         }
@@ -156,21 +173,18 @@ __device__ __forceinline__ void commit(uint64_t *bar) {
 }
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-// 32 columns of the thread's row of an accumulator
-__device__ __forceinline__ void read32(uint32_t at, uint32_t (&r)[32]) {
+// 16 columns of the thread's row of an accumulator; there after read_wait().
+// Both, and add_pair, are volatile, so no use of the values moves before the wait.
+__device__ __forceinline__ void read16(uint32_t at, uint32_t (&r)[16]) {
     asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, "
-        "%23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n\t"
-        "tcgen05.wait::ld.sync.aligned;"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
-          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]),
-          "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]),
-          "=r"(r[30]), "=r"(r[31])
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
         : "r"(at)
         : "memory");
 }
+__device__ __forceinline__ void read_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 // sums of two neighbouring columns: acc += v * s
 __device__ __forceinline__ void add_pair(unsigned long long &acc, uint32_t v0, uint32_t v1, float s) {
     asm volatile("{\n\t.reg .b64 v, s;\n\tmov.b64 v, {%1, %2};\n\tmov.b64 s, {%3, %3};\n\tfma.rn.f32x2 %0, v, s, %0;\n\t}"
@@ -216,9 +230,10 @@ __device__ __forceinline__ Tile tile_of(const ProductParams &p, const int *start
 }
 
 template <bool kGated, bool kGather>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(kGather), 1)
     product_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap wmap,
                    const __grid_constant__ ProductParams p) {
+    constexpr int kThreads = threads_of(kGather);
     extern __shared__ uint8_t smem_raw[];
     __shared__ Barriers bar;
     __shared__ uint32_t s_tmem;
@@ -233,7 +248,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
     if (tid == 0) {
         for (int i = 0; i < kStages; ++i)
-            mbar_init(&bar.full[i], 2 + (kGather ? 2 * kGatherWarps : 0)), mbar_init(&bar.empty[i], 1);
+            mbar_init(&bar.full[i], 3 + (kGather ? 2 * kGatherWarps : 0)), mbar_init(&bar.empty[i], 1);
         for (int i = 0; i < 4; ++i) mbar_init(&bar.tfull[i], 1), mbar_init(&bar.tempty[i], kSums);
         for (int i = 0; i < 4; ++i) mbar_init(&bar.pair[i], 2);
         mbar_fence_init();
@@ -276,20 +291,74 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     fence_after();
     const uint32_t tmem = s_tmem;
     if (warp < 4) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFewRegs));
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLoadRegs));
         int stage = 0;
         uint32_t phase = 0;
         if (warp == 0) {
-            // ---- loads: this CTA's matrix rows, its places' rows where they lie in order, and the
-            // scales, which come four blocks ahead: of four rows a lane, and of the tile's two
-            // matrix blocks, one block of 128 columns to each of eight lanes.
-            int slot = 0;
+            // ---- loads: this CTA's matrix rows, and its places' rows where they lie in order
             for (int id = cluster;; id += clusters) {
                 const Tile t = tile_of(p, start, rank, id);
                 if (!t.any) break;
                 const int pieces = kGather ? 0 : (t.here + 31) / 32;
                 // what both CTAs load: the other one's places too, in whole pieces
                 const int there = kGather ? 0 : (tile_of(p, start, rank ^ 1, id).here + 31) / 32;
+                // 64 matrix rows for each accumulator: the gate's here and the up matrix's there, or the
+                // two halves of a block of 128
+                const int n = kGated ? t.n * kBlock : t.n * kTileN + rank * 64, step_n = kGated ? 64 : kHalfN;
+                for (int kb = 0; kb < p.kb; ++kb) {
+                    if (!wait_for(&bar.empty[stage], phase ^ 1u, &s_stop)) goto done;
+                    uint8_t *a = stages + stage * kStageBytes;
+                    const uint32_t full = first_cta(&bar.full[stage]);
+                    if (lane < 2)
+                        load_4d(a + kABytes + lane * 64 * kBlock, &wmap, kb * kBlock, n + lane * step_n, kGated ? rank : 0,
+                                t.expert, full);
+                    if (!kGather && lane < pieces)
+                        load_2d(a + lane * 32 * kBlock, &amap, kb * kBlock, t.first + lane * 32, full);
+                    if (rank == 0 && lane == 0)
+                        mbar_arrive_expect_tx(&bar.full[stage], 2 * kBBytes + (pieces + there) * 32 * kBlock);
+                    __syncwarp();
+                    if (++stage == kStages) stage = 0, phase ^= 1u;
+                }
+            }
+            // let what is in flight land: every stage that was filled is emptied by the multiplier
+            for (int i = 0; i < kStages; ++i) {
+                if (!wait_for(&bar.empty[stage], phase ^ 1u, &s_stop)) break;
+                if (++stage == kStages) stage = 0, phase ^= 1u;
+            }
+        } else if (warp == 1) {
+            // ---- products, by one thread of the first CTA: a block of 128 columns into an accumulator
+            // for each half of the tile's columns; two turns of them
+            if (rank == 0 && elected()) {
+                uint32_t step = 0;
+                const uint32_t steps = static_cast<uint32_t>((start[p.experts] - cluster + clusters - 1) / clusters) * p.kb;
+                for (bool ok = true; ok && step < steps; ++step) {
+                    ok = wait_alone(&bar.full[stage], phase, &s_stop);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int buf = (step & 1) * 2 + h;
+                        ok = ok && wait_alone(&bar.tempty[buf], ((step >> 1) & 1) ^ 1u, &s_stop);
+                        if (ok) {
+                            fence_after();
+                            const uint64_t a = operand(stages + stage * kStageBytes);
+                            const uint64_t b = operand(stages + stage * kStageBytes + kABytes + h * 64 * kBlock);
+#pragma unroll
+                            for (int k = 0; k < kBlock / 32; ++k)       // 32 columns an instruction: 2 units of 16 bytes
+                                multiply(tmem + buf * kHalfN, a + 2 * k, b + 2 * k, k > 0);
+                            commit(&bar.tfull[buf]);
+                        }
+                    }
+                    if (ok) commit(&bar.empty[stage]);
+                    if (++stage == kStages) stage = 0, phase ^= 1u;
+                }
+            }
+            __syncwarp();
+        } else if (warp == 2) {
+            // ---- scales, which come four blocks ahead: of four rows a lane, and of the tile's two matrix
+            // blocks, one block of 128 columns to each of eight lanes
+            int slot = 0;
+            for (int id = cluster;; id += clusters) {
+                const Tile t = tile_of(p, start, rank, id);
+                if (!t.any) break;
                 const float *sa[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
@@ -333,123 +402,72 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     scales(k0 + 4);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const int kb = k0 + i;
-                        if (kb >= p.kb) break;
+                        if (k0 + i >= p.kb) break;
                         if (!wait_for(&bar.empty[stage], phase ^ 1u, &s_stop)) goto done;
-                        uint8_t *a = stages + stage * kStageBytes;
-                        const uint32_t full = first_cta(&bar.full[stage]);
-                        if (lane == 0) {
-                            // 64 matrix rows for each accumulator: the gate's here and the up matrix's
-                            // there, or the two halves of a block of 128
-#pragma unroll
-                            for (int h = 0; h < 2; ++h) {
-                                const int n = kGated ? t.n * kBlock + h * 64 : t.n * kTileN + h * kHalfN + rank * 64;
-                                load_4d(a + kABytes + h * 64 * kBlock, &wmap, kb * kBlock, n, kGated ? rank : 0, t.expert,
-                                        full);
-                            }
-                        }
-                        __syncwarp();
-                        if (!kGather && lane < pieces)
-                            load_2d(a + lane * 32 * kBlock, &amap, kb * kBlock, t.first + lane * 32, full);
 #pragma unroll
                         for (int j = 0; j < 4; ++j) s_x[slot][j * 32 + lane] = xs[j][i];
                         if (lane < 8 && (lane & 3) == i) s_w[slot][lane >> 2] = ws;
                         __syncwarp();
-                        if (lane == 0) {
-                            if (rank == 0)
-                                mbar_arrive_expect_tx(&bar.full[stage], 2 * kBBytes + (pieces + there) * 32 * kBlock);
-                            else
-                                arrive_cluster(full);
-                        }
+                        // the sums learn of it by way of the step's products (a barrier of their own for
+                        // it made a step of 0.51 us take 0.56)
+                        if (lane == 0) arrive_cluster(first_cta(&bar.full[stage]));
                         slot = (slot + 1) % kSlots;
                         if (++stage == kStages) stage = 0, phase ^= 1u;
                     }
                 }
             }
-            // let what is in flight land: every stage that was filled is emptied by the multiplier
-            for (int i = 0; i < kStages; ++i) {
-                if (!wait_for(&bar.empty[stage], phase ^ 1u, &s_stop)) break;
+        }
+    } else if (kGather && warp >= 4 + kSums) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kGatherRegs));
+        // ---- places' rows from anywhere: eight threads a row of 128 bytes, kGatherRows rows a thread.
+        // A stage is handed over kGatherLag blocks later, when its copies are complete.
+        constexpr int kStride = kGatherWarps * 4;        // rows that the warps fetch at once
+        const int i = tid - 32 * (4 + kSums), sub = i >> 3, seg = i & 7;
+        const uint8_t *base = p.a_rows > 0 ? p.values : p.w;
+        int stage = 0, lagging = 0, late = 0;       // stages not yet handed over, the first of them
+        uint32_t phase = 0;
+        for (int id = cluster;; id += clusters) {
+            const Tile t = tile_of(p, start, rank, id);
+            if (!t.any) break;
+            int src[kGatherRows];
+#pragma unroll
+            for (int j = 0; j < kGatherRows; ++j) {
+                src[j] = sub + kStride * j < t.here ? p.rows[t.first + sub + kStride * j] : -1;
+                if (src[j] >= p.a_rows) src[j] = -1;
+            }
+            const int steps = (t.here + kStride - 1) / kStride;
+            for (int kb = 0; kb < p.kb; ++kb) {
+                if (!wait_for(&bar.empty[stage], phase ^ 1u, &s_stop)) goto done;
+                const uint32_t to = smem_u32(stages + stage * kStageBytes) + sub * 128 + ((seg ^ (sub & 7)) << 4);
+                const int col = kb * kBlock + seg * 16;
+#pragma unroll
+                for (int j = 0; j < kGatherRows; ++j)
+                    if (j < steps) {
+                        const bool there = src[j] >= 0 && col < p.width;
+                        fetch16(to + j * kStride * 128, there ? base + src[j] * p.value_stride + col : base, there);
+                    }
+                asm volatile("cp.async.commit_group;" ::: "memory");
+                if (lagging == kGatherLag) {
+                    asm volatile("cp.async.wait_group %0;" ::"n"(kGatherLag) : "memory");
+                    fence_proxy_async_shared();
+                    __syncwarp();
+                    if (lane == 0) arrive_cluster(first_cta(&bar.full[late]));
+                    if (++late == kStages) late = 0;
+                } else {
+                    ++lagging;
+                }
                 if (++stage == kStages) stage = 0, phase ^= 1u;
             }
-        } else if (warp == 1) {
-            // ---- products, by the first CTA: a block of 128 columns into an accumulator for each
-            // half of the tile's columns; two turns of them
-            int turn = 0;
-            uint32_t tphase = 0;
-            const int total = rank == 0 ? start[p.experts] : 0;
-            for (int id = cluster; id < total; id += clusters) {
-                for (int kb = 0; kb < p.kb; ++kb) {
-                    if (!wait_for(&bar.full[stage], phase, &s_stop)) goto done;
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const int buf = turn * 2 + h;
-                        if (!wait_for(&bar.tempty[buf], tphase ^ 1u, &s_stop)) goto done;
-                        fence_after();
-                        if (elected()) {
-                            const uint64_t a = operand(stages + stage * kStageBytes);
-                            const uint64_t b = operand(stages + stage * kStageBytes + kABytes + h * 64 * kBlock);
-#pragma unroll
-                            for (int k = 0; k < kBlock / 32; ++k)       // 32 columns an instruction: 2 units of 16 bytes
-                                multiply(tmem + buf * kHalfN, a + 2 * k, b + 2 * k, k > 0);
-                            commit(&bar.tfull[buf]);
-                            if (h == 1) commit(&bar.empty[stage]);
-                        }
-                        __syncwarp();
-                    }
-                    if (++stage == kStages) stage = 0, phase ^= 1u;
-                    turn ^= 1;
-                    if (turn == 0) tphase ^= 1u;
-                }
-            }
-        } else if (kGather) {
-            // ---- places' rows from anywhere: eight threads a row of 128 bytes, 16 rows a thread.
-            // A stage is handed over kGatherLag blocks later, when its copies are complete.
-            const int i = tid - 64, sub = i >> 3, seg = i & 7;
-            const uint8_t *base = p.a_rows > 0 ? p.values : p.w;
-            int lagging = 0, late = 0;       // stages not yet handed over, the first of them
-            for (int id = cluster;; id += clusters) {
-                const Tile t = tile_of(p, start, rank, id);
-                if (!t.any) break;
-                int src[16];
-#pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    src[j] = sub + 8 * j < t.here ? p.rows[t.first + sub + 8 * j] : -1;
-                    if (src[j] >= p.a_rows) src[j] = -1;
-                }
-                const int steps = (t.here + 7) / 8;
-                for (int kb = 0; kb < p.kb; ++kb) {
-                    if (!wait_for(&bar.empty[stage], phase ^ 1u, &s_stop)) goto done;
-                    const uint32_t to = smem_u32(stages + stage * kStageBytes) + sub * 128 + ((seg ^ sub) << 4);
-                    const int col = kb * kBlock + seg * 16;
-#pragma unroll
-                    for (int j = 0; j < 16; ++j)
-                        if (j < steps) {
-                            const bool there = src[j] >= 0 && col < p.width;
-                            fetch16(to + j * 1024, there ? base + src[j] * p.value_stride + col : base, there);
-                        }
-                    asm volatile("cp.async.commit_group;" ::: "memory");
-                    if (lagging == kGatherLag) {
-                        asm volatile("cp.async.wait_group %0;" ::"n"(kGatherLag) : "memory");
-                        fence_proxy_async_shared();
-                        __syncwarp();
-                        if (lane == 0) arrive_cluster(first_cta(&bar.full[late]));
-                        if (++late == kStages) late = 0;
-                    } else {
-                        ++lagging;
-                    }
-                    if (++stage == kStages) stage = 0, phase ^= 1u;
-                }
-            }
-            asm volatile("cp.async.wait_group 0;" ::: "memory");
-            fence_proxy_async_shared();
-            __syncwarp();
-            for (; lagging > 0; --lagging) {
-                if (lane == 0) arrive_cluster(first_cta(&bar.full[late]));
-                if (++late == kStages) late = 0;
-            }
+        }
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        fence_proxy_async_shared();
+        __syncwarp();
+        for (; lagging > 0; --lagging) {
+            if (lane == 0) arrive_cluster(first_cta(&bar.full[late]));
+            if (++late == kStages) late = 0;
         }
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kManyRegs));
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(sum_regs(kGather)));
         // ---- sums: accumulator times the two scales, added up in registers.
         // A warp reads the 32 rows that its number allows, and one half's
         // accumulators: a block of 128 columns, or 64 of the gate's and the same 64
@@ -457,6 +475,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int quad = warp & 3, half = (warp - 4) >> 2, row = quad * 32 + lane;
         int turn = 0;
         uint32_t step = 0;
+        auto accumulator_read = [&](int buf) {
+            fence_before();
+            __syncwarp();
+            if (lane == 0) arrive_cluster(first_cta(&bar.tempty[buf]));
+        };
         for (int id = cluster;; id += clusters) {
             const Tile cur = tile_of(p, start, rank, id);
             if (!cur.any) break;
@@ -467,24 +490,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll 1
             for (int kb = 0; kb < p.kb; ++kb, ++step) {
                 const int buf = half + 2 * (step & 1);       // this warp's accumulators: half, and half + 2
-                if (!wait_for(&bar.tfull[buf], (step >> 1) & 1, &s_stop)) goto done;
+                                if (!wait_for(&bar.tfull[buf], (step >> 1) & 1, &s_stop)) goto done;
                 fence_after();
                 if (active) {
+                    // 16 columns are read while the last 16 are added
+                    const uint32_t at = tmem + (static_cast<uint32_t>(quad * 32) << 16) + buf * kHalfN;
+                    uint32_t v[2][16];
+                    read16(at, v[0]);
                     const float x = s_x[step % kSlots][row];
                     const float s0 = x * s_w[step % kSlots][kGated ? 0 : half], s1 = kGated ? x * s_w[step % kSlots][1] : s0;
-                    const uint32_t at = tmem + (static_cast<uint32_t>(quad * 32) << 16) + buf * kHalfN;
-                    uint32_t v[32];
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        read32(at + c * 32, v);
+                    for (int c = 0; c < 8; ++c) {
+                        read_wait();
+                        if (c < 7) read16(at + (c + 1) * 16, v[(c + 1) & 1]);
+                        else accumulator_read(buf);
 #pragma unroll
-                        for (int q = 0; q < 16; ++q)
-                            add_pair(acc[c * 16 + q], v[2 * q], v[2 * q + 1], c < 2 ? s0 : s1);
+                        for (int q = 0; q < 8; ++q)
+                            add_pair(acc[c * 8 + q], v[c & 1][2 * q], v[c & 1][2 * q + 1], c < 4 ? s0 : s1);
                     }
+                } else {
+                    accumulator_read(buf);
                 }
-                fence_before();
-                __syncwarp();
-                if (lane == 0) arrive_cluster(first_cta(&bar.tempty[buf]));
             }
             const bool mine = row < cur.here;
             const int64_t place = cur.first + row;
@@ -618,7 +644,7 @@ ep_status launch_product(const ProductParams &p, int device, cudaStream_t st) {
     // every expert may leave one tile short
     const int64_t tiles = (p.places / kTileM + (p.places < p.experts ? p.places : p.experts)) * ntiles;
     const unsigned grid = 2 * static_cast<unsigned>(tiles < sms / 2 ? tiles : sms / 2);
-    product_kernel<kGated, kGather><<<grid, kThreads, smem, st>>>(amap, wmap, p);
+    product_kernel<kGated, kGather><<<grid, threads_of(kGather), smem, st>>>(amap, wmap, p);
     return launched();
 }
 
