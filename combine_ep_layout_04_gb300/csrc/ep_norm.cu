@@ -117,9 +117,9 @@ struct NormGradParams {
 
 // A team keeps its columns' sums of dout * u in registers over all its rows
 // (rows team, team + teams, ...) and writes them once; dweight_kernel adds the
-// teams' sums in order.
+// teams' sums in order.  All three rows are asked for before anything waits.
 template <int VPT, bool kWide>
-__global__ void __launch_bounds__(kWide ? 1024 : 32 * kTeams) norm_grad_kernel(NormGradParams p) {
+__global__ void __launch_bounds__(kWide ? 1024 : 32 * kTeams, kWide ? 1 : 3) norm_grad_kernel(NormGradParams p) {
     __shared__ float part[2][32];
     const int64_t team = kWide ? blockIdx.x : static_cast<int64_t>(blockIdx.x) * kTeams + (threadIdx.x >> 5);
     const int64_t teams = kWide ? gridDim.x : static_cast<int64_t>(gridDim.x) * kTeams;
@@ -134,15 +134,16 @@ __global__ void __launch_bounds__(kWide ? 1024 : 32 * kTeams) norm_grad_kernel(N
     int turn = 0;
     for (int64_t t = team; t < p.tokens; t += teams, turn ^= 1) {
         const float rstd = p.rstd[t];
-        uint4 d[VPT], s[VPT];
+        uint4 d[VPT], s[VPT], e[VPT];
         float sum = 0.0f;
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             const int v = i * width + lane;
-            d[i] = s[i] = make_uint4(0, 0, 0, 0);
+            d[i] = s[i] = e[i] = make_uint4(0, 0, 0, 0);
             if (v < nvec) {
                 d[i] = *reinterpret_cast<const uint4 *>(p.dout + t * p.dout_stride + v * 8);
                 s[i] = *reinterpret_cast<const uint4 *>(p.h + t * p.h_stride + v * 8);
+                if (p.dresidual) e[i] = *reinterpret_cast<const uint4 *>(p.dresidual + t * p.dresidual_stride + v * 8);
             }
         }
 #pragma unroll
@@ -170,11 +171,8 @@ __global__ void __launch_bounds__(kWide ? 1024 : 32 * kTeams) norm_grad_kernel(N
                 float g[8], u[8], w[8], r[8];
                 unpack8(d[i], g);
                 unpack8(s[i], u);
+                unpack8(e[i], r);
                 load8(p.weight, p.weight_dtype, v * 8, w);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) r[j] = 0.0f;
-                if (p.dresidual)
-                    unpack8(*reinterpret_cast<const uint4 *>(p.dresidual + t * p.dresidual_stride + v * 8), r);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) r[j] = fmaf(rstd, fmaf(g[j], w[j], -(u[j] * rstd) * mean), r[j]);
                 *reinterpret_cast<uint4 *>(p.dx + t * p.dx_stride + v * 8) = pack8(r);
@@ -207,24 +205,27 @@ __global__ void __launch_bounds__(1024) dweight_kernel(const float *part, int te
 }
 
 // How a row is held: VPT steps of 8 columns a lane, and the warps of a block
-// (one warp to a row where wide is false).
+// (one warp to a row where wide is false).  Up to `most` steps a lane: four
+// forward, two backward, where a lane holds three rows and the sums.
 struct Shape {
     int vpt, warps;
     bool wide;
-    explicit Shape(int hidden) {
+    Shape(int hidden, int most) {
         const int nvec = hidden / 8;
-        wide = nvec > 128;
-        vpt = nvec > 64 ? 4 : nvec > 32 ? 2 : 1;
-        warps = wide ? (nvec + 127) / 128 : kTeams;
+        wide = nvec > 32 * most;
+        vpt = nvec > 64 && most > 2 ? 4 : nvec > 32 ? 2 : 1;
+        if (wide && nvec > 32 * 32 * most) vpt = 4;      // a block has 32 warps at most
+        else if (wide) vpt = most;
+        warps = wide ? (nvec + 32 * vpt - 1) / (32 * vpt) : kTeams;
     }
     int rows_per_block() const { return wide ? 1 : kTeams; }
 };
 
-// Blocks of the backward kernel: about four a SM where a block is small, so
+// Blocks of the backward kernel: as many as run at once (24 warps an SM), so
 // that a team keeps its sums over as many rows as it can.
 int grad_blocks(int64_t tokens, int hidden, int sms) {
-    const Shape s(hidden);
-    const int per_sm = s.warps <= 8 ? 4 : s.warps <= 16 ? 2 : 1;
+    const Shape s(hidden, 2);
+    const int per_sm = s.warps >= 24 ? 1 : 24 / s.warps;
     const int64_t rows = (tokens + s.rows_per_block() - 1) / s.rows_per_block();
     return static_cast<int>(rows < static_cast<int64_t>(sms) * per_sm ? rows : static_cast<int64_t>(sms) * per_sm);
 }
@@ -269,7 +270,7 @@ ep_status ep_rms_norm(int64_t tokens, int32_t hidden, const void *x, int64_t x_s
     p.scales = scales, p.scale_stride = scale_stride;
     p.residual_out = static_cast<__nv_bfloat16 *>(residual_out), p.residual_out_stride = residual_out_stride;
     p.rstd = rstd, p.hidden = hidden, p.eps = eps;
-    const Shape s(hidden);
+    const Shape s(hidden, 4);
     const unsigned grid = static_cast<unsigned>((tokens + s.rows_per_block() - 1) / s.rows_per_block());
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (s.wide)
@@ -286,7 +287,7 @@ ep_status ep_rms_norm(int64_t tokens, int32_t hidden, const void *x, int64_t x_s
 int64_t ep_rms_norm_backward_workspace(int64_t tokens, int32_t hidden) {
     if (tokens < 0 || tokens >= (1ll << 31) || hidden < 8 || hidden % 8 != 0 || hidden > kMaxHidden) return 0;
     // enough for any device: 256 SMs (a grid is cut to what the workspace holds)
-    return static_cast<int64_t>(grad_blocks(tokens, hidden, 256)) * Shape(hidden).rows_per_block() * hidden * 4;
+    return static_cast<int64_t>(grad_blocks(tokens, hidden, 256)) * Shape(hidden, 2).rows_per_block() * hidden * 4;
 }
 
 ep_status ep_rms_norm_backward(int64_t tokens, int32_t hidden, const void *dout, int64_t dout_stride, const void *h,
@@ -323,12 +324,12 @@ ep_status ep_rms_norm_backward(int64_t tokens, int32_t hidden, const void *dout,
     p.weight = weight, p.weight_dtype = weight_dtype, p.rstd = rstd;
     p.dx = static_cast<__nv_bfloat16 *>(dx), p.dx_stride = dx_stride;
     p.part = static_cast<float *>(workspace), p.hidden = hidden;
-    const Shape s(hidden);
+    const Shape s(hidden, 2);
     const int grid = grad_blocks(tokens, hidden, sms < 256 ? sms : 256);
-    if (s.wide)
+    if (s.wide && s.vpt == 4)
         norm_grad_kernel<4, true><<<grid, 32 * s.warps, 0, st>>>(p);
-    else if (s.vpt == 4)
-        norm_grad_kernel<4, false><<<grid, 32 * kTeams, 0, st>>>(p);
+    else if (s.wide)
+        norm_grad_kernel<2, true><<<grid, 32 * s.warps, 0, st>>>(p);
     else if (s.vpt == 2)
         norm_grad_kernel<2, false><<<grid, 32 * kTeams, 0, st>>>(p);
     else

@@ -3,9 +3,15 @@
 // gradient (include/ep_ops.h).
 //
 // A warp holds a token's logits in registers, VPT to a lane, expert
-// j * 32 + lane in step j.  Logits are compared as whole numbers in the floats'
-// order, 0 for what is never picked, so that one warp-wide integer maximum
-// finds a pick and one minimum over the lanes' expert ids settles ties.
+// j * 32 + lane in step j.  Its K largest are found without sorting:
+//  - each lane's largest logit is known, and the K-th largest of these 32 (K
+//    warp-wide maxima) is a bound that at least K logits reach;
+//  - the few logits that reach it -- about K + 2 of 256 -- are written to
+//    shared memory as 64-bit words, the logit's bits in the floats' order and
+//    then the expert, so that ties go to the lower one;
+//  - each of them counts the words above its own: that is its place.
+// About 250 instructions a token and warp, where K rounds of a maximum over
+// all logits took 1800 (131072 tokens of 256 logits: 207 us, all issue).
 #include <type_traits>
 
 #include "ep_ops.cuh"
@@ -30,9 +36,6 @@ struct RouteParams {
     int experts, topk, renormalize, per_rank, bf16;
 };
 
-__device__ __forceinline__ float load_logit(const void *p, int bf16, int64_t at) {
-    return bf16 ? __bfloat162float(static_cast<const __nv_bfloat16 *>(p)[at]) : static_cast<const float *>(p)[at];
-}
 // Whole numbers in the order of the floats; 0 for -inf and NaN, which are
 // never picked (every other float gives more than 0).
 __device__ __forceinline__ uint32_t order_key(float v) {
@@ -43,9 +46,93 @@ __device__ __forceinline__ float key_value(uint32_t k) {
     return __uint_as_float((k & 0x80000000u) ? k & 0x7fffffffu : ~k);
 }
 
+constexpr int kWords = 64;         // words of a warp's list; a longer one (ties, wide K) takes the slow way
+
+__device__ __forceinline__ unsigned long long pick_word(float l, int e) {
+    return (static_cast<unsigned long long>(order_key(l)) << 32) | static_cast<uint32_t>(~e);
+}
+
+// Loads a lane's logits; what lies past the experts is -inf.
+template <int VPT>
+__device__ __forceinline__ void load_row(const void *logits, int bf16, int64_t at, int experts, int lane, float (&l)[VPT]) {
+    if (bf16) {
+        const __nv_bfloat16 *row = static_cast<const __nv_bfloat16 *>(logits) + at;
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) l[j] = j * 32 + lane < experts ? __bfloat162float(row[j * 32 + lane]) : -INFINITY;
+    } else {
+        const float *row = static_cast<const float *>(logits) + at;
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) l[j] = j * 32 + lane < experts ? row[j * 32 + lane] : -INFINITY;
+    }
+}
+
+// Lane k gets pick k's word, 0 where there is none; `top`: the largest key.
+template <int VPT>
+__device__ __forceinline__ unsigned long long pick(const float (&l)[VPT], int K, int lane, unsigned long long *words,
+                                                   unsigned long long *picks, uint32_t &top) {
+    float most = l[0];
+#pragma unroll
+    for (int j = 1; j < VPT; ++j) most = fmaxf(most, l[j]);      // NaN is passed over
+    uint32_t left = order_key(most), bound = 0;
+    top = __reduce_max_sync(0xffffffffu, left);
+    for (int k = 0; k < K; ++k) {
+        bound = k == 0 ? top : __reduce_max_sync(0xffffffffu, left);
+        if (bound == 0) break;
+        left = left == bound ? 0u : left;
+    }
+    // fewer than K different maxima: every logit above -inf is on the list
+    const float least = bound ? key_value(bound) : -3.402823466e38f;
+    int n = 0;
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+        const bool on = l[j] >= least;
+        const uint32_t lanes = __ballot_sync(0xffffffffu, on);
+        const int at = n + __popc(lanes & ((1u << lane) - 1u));
+        if (on && at < kWords) words[at] = pick_word(l[j], j * 32 + lane);
+        n += __popc(lanes);
+    }
+    __syncwarp();
+    unsigned long long mine = 0;
+    if (n <= kWords) {
+        const unsigned long long a = lane < n ? words[lane] : 0, b = lane + 32 < n ? words[lane + 32] : 0;
+        int above_a = 0, above_b = 0;
+        for (int q = 0; q < n; ++q) {
+            const unsigned long long w = words[q];
+            above_a += w > a;
+            above_b += w > b;
+        }
+        if (a && above_a < K) picks[above_a] = a;
+        if (b && above_b < K) picks[above_b] = b;
+        __syncwarp();
+        if (lane < K && lane < n) mine = picks[lane];
+        __syncwarp();
+    } else {
+        // one pick after another: the largest word below the last pick
+        unsigned long long last = ~0ull;
+        for (int k = 0; k < K; ++k) {
+            unsigned long long best = 0;
+#pragma unroll
+            for (int j = 0; j < VPT; ++j) {
+                const unsigned long long w = l[j] > -INFINITY ? pick_word(l[j], j * 32 + lane) : 0;
+                if (w < last && w > best) best = w;
+            }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) {
+                const unsigned long long w = __shfl_xor_sync(0xffffffffu, best, o);
+                best = w > best ? w : best;
+            }
+            if (best == 0) break;
+            if (lane == k) mine = best;
+            last = best;
+        }
+    }
+    return mine;
+}
+
 template <int VPT, bool kTrain>
 __global__ void __launch_bounds__(32 * kWarps) route_kernel(RouteParams p) {
     extern __shared__ float smem[];      // kTrain: p sums [kWarps][experts], then counts [experts]
+    __shared__ unsigned long long s_words[kWarps][kWords], s_picks[kWarps][kMaxTopk];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int E = p.experts, K = p.topk;
     int32_t *count = reinterpret_cast<int32_t *>(smem + (kTrain ? kWarps * E : 0));
@@ -62,43 +149,23 @@ __global__ void __launch_bounds__(32 * kWarps) route_kernel(RouteParams p) {
         const bool live = p.mask == nullptr || p.mask[t] != 0;
         live_tokens += live;
         float l[VPT];
-        uint32_t best = 0;
-        int best_e = 0;
-#pragma unroll
-        for (int j = 0; j < VPT; ++j) {
-            const int e = j * 32 + lane;
-            l[j] = live && e < E ? load_logit(p.logits, p.bf16, t * p.logits_stride + e) : -INFINITY;
-            const uint32_t k = order_key(l[j]);
-            if (k > best) best = k, best_e = e;
-        }
-        const uint32_t top = __reduce_max_sync(0xffffffffu, best);
+        load_row(p.logits, p.bf16, t * p.logits_stride, live ? E : 0, lane, l);
+        uint32_t top;
+        const unsigned long long word = pick(l, K, lane, s_words[warp], s_picks[warp], top);
+        const int my_e = word ? static_cast<int>(~static_cast<uint32_t>(word)) : -1;
         const float most = top ? key_value(top) : 0.0f;
         float sum = 0.0f;
+        if (kTrain || !p.renormalize) {
 #pragma unroll
-        for (int j = 0; j < VPT; ++j) sum += j * 32 + lane < E ? expf(l[j] - most) : 0.0f;
-        sum = warp_sum(sum);       // 0 if no logit is left, NaN if one is NaN
-        // the picks, largest first; lane k keeps pick k
-        uint32_t taken[(VPT + 31) / 32] = {};
-        int my_e = -1;
-        float my_l = -INFINITY;
-        for (int k = 0; k < K; ++k) {
-            const uint32_t m = __reduce_max_sync(0xffffffffu, best);
-            if (m == 0) break;
-            const int e = __reduce_min_sync(0xffffffffu, best == m ? best_e : kMaxExperts);
-            if (lane == k) my_e = e, my_l = key_value(m);
-            if ((e & 31) == lane) {
-                best = 0;
-#pragma unroll
-                for (int j = 0; j < VPT; ++j) {
-                    if (j == e >> 5) taken[j / 32] |= 1u << (j & 31);
-                    const uint32_t key = (taken[j / 32] >> (j & 31)) & 1u ? 0u : order_key(l[j]);
-                    if (key > best) best = key, best_e = j * 32 + lane;
-                }
+            for (int j = 0; j < VPT; ++j) {
+                l[j] = __expf(l[j] - most);
+                sum += l[j];
             }
+            sum = warp_sum(sum);       // 0 if no logit is left, NaN if one is NaN
         }
-        float w = my_e >= 0 ? expf(my_l - most) : 0.0f;
+        float w = word ? __expf(key_value(static_cast<uint32_t>(word >> 32)) - most) : 0.0f;
         const float total = p.renormalize ? warp_sum(w) : sum;
-        w = my_e >= 0 ? w / total : 0.0f;
+        w = word ? w / total : 0.0f;
         if (lane < K) {
             p.topk_idx[t * K + lane] = my_e;
             p.topk_weights[t * K + lane] = w;
@@ -113,8 +180,7 @@ __global__ void __launch_bounds__(32 * kWarps) route_kernel(RouteParams p) {
             if (lane == 0) p.lse[t] = live ? (top ? most + logf(sum) : sum != sum ? sum : -INFINITY) : INFINITY;
             const float inv = sum != 0.0f ? 1.0f / sum : 0.0f;
 #pragma unroll
-            for (int j = 0; j < VPT; ++j)
-                if (j * 32 + lane < E) psum[j] += expf(l[j] - most) * inv;
+            for (int j = 0; j < VPT; ++j) psum[j] = fmaf(l[j], inv, psum[j]);
         }
     }
     if (kTrain) {
@@ -139,27 +205,46 @@ __global__ void __launch_bounds__(32 * kWarps) route_kernel(RouteParams p) {
 }
 
 // Adds the blocks' sums in order and makes counts, slope and loss; one block.
+// Up to 1024 / experts threads share an expert, each takes every so many
+// blocks, and their sums are added in order.
 __global__ void __launch_bounds__(1024) balance_kernel(const float *part_p, const int32_t *part_count,
                                                        const int32_t *part_live, int parts, int experts, int topk,
                                                        float coef, int32_t *expert_count, float *loss, float *slope) {
-    __shared__ float sums[32];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    __shared__ float sums[32], s_p[1024];
+    __shared__ int s_live[32], s_n[1024];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     int live = 0;
-    for (int b = 0; b < parts; ++b) live += part_live[b];
+    for (int b = tid; b < parts; b += 1024) live += part_live[b];
+    live = __reduce_add_sync(0xffffffffu, live);
+    if (lane == 0) s_live[warp] = live;
+    __syncthreads();
+    live = __reduce_add_sync(0xffffffffu, s_live[lane]);
     const float tv = live > 0 ? static_cast<float>(live) : 1.0f;
     const float scale = coef * static_cast<float>(experts) / (static_cast<float>(topk) * tv * tv);
+    const int share = experts < 1024 ? 1024 / experts : 1, span = experts < 1024 ? experts : 1024;
     float sum = 0.0f;
-    for (int e = threadIdx.x; e < experts; e += blockDim.x) {
+    for (int e0 = 0; e0 < experts; e0 += span) {
+        const int e = e0 + tid % span, g = tid / span;
         float s = 0.0f;
         int n = 0;
-        for (int b = 0; b < parts; ++b) {
-            s += part_p[static_cast<int64_t>(b) * experts + e];
-            n += part_count[static_cast<int64_t>(b) * experts + e];
+        if (e < experts && g < share) {
+#pragma unroll 8
+            for (int b = g; b < parts; b += share) {
+                s += part_p[static_cast<int64_t>(b) * experts + e];
+                n += part_count[static_cast<int64_t>(b) * experts + e];
+            }
         }
-        const float g = scale * static_cast<float>(n);
-        expert_count[e] = n;
-        slope[e] = g;
-        sum += g * s;
+        __syncthreads();
+        s_p[tid] = s;
+        s_n[tid] = n;
+        __syncthreads();
+        if (g == 0 && e < experts) {
+            for (int i = 1; i < share; ++i) s += s_p[i * span + tid], n += s_n[i * span + tid];
+            const float slope_e = scale * static_cast<float>(n);
+            expert_count[e] = n;
+            slope[e] = slope_e;
+            sum += slope_e * s;
+        }
     }
     sum = warp_sum(sum);
     if (lane == 0) sums[warp] = sum;
@@ -183,71 +268,73 @@ struct RouteGradParams {
 // dl_e = p_e (g_e - <p, g>) + picks.  Renormalised weights depend on the
 // picked logits alone: a pick's logit gets w (dw - <w, dw>).  Otherwise a
 // weight is its p, and dw joins g.
+// The picks' parts go through a row of shared memory that is zero between tokens.
 template <int VPT>
 __global__ void __launch_bounds__(32 * kWarps) route_grad_kernel(RouteGradParams p) {
+    extern __shared__ float smem[];      // [kWarps][experts]
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int E = p.experts, K = p.topk;
-    const int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
-    if (t >= p.tokens) return;
+    float *picks = smem + warp * E;
+    for (int e = lane; e < E; e += 32) picks[e] = 0.0f;
+    __syncwarp();
     const float dloss = p.dloss ? *p.dloss : 0.0f;
-    const float lse = p.lse[t];
-    const bool live = !isinf(lse);       // +inf: a padded token, -inf: no logit left; both have p = 0
-    int idx = -1;
-    float w = 0.0f, add = 0.0f;
-    if (lane < K) {
-        idx = p.topk_idx[t * K + lane];
-        if (idx >= 0) {
-            w = p.topk_weights[t * K + lane];
-            add = p.dweights[t * K + lane];
-        }
+    constexpr bool kHeld = VPT <= 16;    // the slope stays in registers
+    float slope[kHeld ? VPT : 1];
+    if (kHeld) {
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) slope[j] = p.dloss && j * 32 + lane < E ? dloss * p.slope[j * 32 + lane] : 0.0f;
     }
-    if (p.renormalize) {
-        const float mean = warp_sum(w * add);
-        add = w * (add - mean);
-    }
-    float prob[VPT], g[VPT], inner = 0.0f;
-#pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-        const int e = j * 32 + lane;
-        prob[j] = live && e < E ? expf(load_logit(p.logits, p.bf16, t * p.logits_stride + e) - lse) : 0.0f;
-        g[j] = live && e < E && p.dloss ? dloss * p.slope[e] : 0.0f;
-    }
-    if (!p.renormalize)
-        for (int k = 0; k < K; ++k) {
-            const int e = __shfl_sync(0xffffffffu, idx, k);
-            const float a = __shfl_sync(0xffffffffu, add, k);
-#pragma unroll
-            for (int j = 0; j < VPT; ++j)
-                if (e == j * 32 + lane) g[j] += a;
+    for (int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + warp; t < p.tokens;
+         t += static_cast<int64_t>(gridDim.x) * kWarps) {
+        const float lse = p.lse[t];
+        const bool live = !isinf(lse);       // +inf: a padded token, -inf: no logit left; both have p = 0
+        float l[VPT];
+        load_row(p.logits, p.bf16, t * p.logits_stride, live ? E : 0, lane, l);
+        int idx = -1;
+        float w = 0.0f, add = 0.0f;
+        if (lane < K) {
+            idx = p.topk_idx[t * K + lane];
+            if (idx >= 0) {
+                w = p.topk_weights[t * K + lane];
+                add = p.dweights[t * K + lane];
+            }
         }
+        if (p.renormalize) add = w * (add - warp_sum(w * add));
+        if (idx >= 0 && idx < E) picks[idx] = add;
+        __syncwarp();
+        float g[VPT], inner = 0.0f;
 #pragma unroll
-    for (int j = 0; j < VPT; ++j) inner = fmaf(prob[j], g[j], inner);
-    inner = warp_sum(inner);
-#pragma unroll
-    for (int j = 0; j < VPT; ++j) g[j] = prob[j] * (g[j] - inner);
-    if (p.renormalize)
-        for (int k = 0; k < K; ++k) {
-            const int e = __shfl_sync(0xffffffffu, idx, k);
-            const float a = __shfl_sync(0xffffffffu, add, k);
-#pragma unroll
-            for (int j = 0; j < VPT; ++j)
-                if (e == j * 32 + lane) g[j] += a;
+        for (int j = 0; j < VPT; ++j) {
+            const int e = j * 32 + lane;
+            l[j] = live ? __expf(l[j] - lse) : 0.0f;
+            g[j] = kHeld ? slope[j] : p.dloss && e < E ? dloss * p.slope[e] : 0.0f;
+            if (!p.renormalize && e < E) g[j] += picks[e];
+            inner = fmaf(l[j], g[j], inner);
         }
+        inner = warp_sum(inner);
 #pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-        const int e = j * 32 + lane;
-        if (e < E) {
-            if (p.bf16)
-                static_cast<__nv_bfloat16 *>(p.dlogits)[t * p.dlogits_stride + e] = __float2bfloat16(g[j]);
-            else
-                static_cast<float *>(p.dlogits)[t * p.dlogits_stride + e] = g[j];
+        for (int j = 0; j < VPT; ++j) {
+            const int e = j * 32 + lane;
+            if (e < E) {
+                const float d = l[j] * (g[j] - inner) + (p.renormalize ? picks[e] : 0.0f);
+                if (p.bf16)
+                    static_cast<__nv_bfloat16 *>(p.dlogits)[t * p.dlogits_stride + e] = __float2bfloat16(d);
+                else
+                    static_cast<float *>(p.dlogits)[t * p.dlogits_stride + e] = d;
+            }
         }
+        __syncwarp();
+        if (idx >= 0 && idx < E) picks[idx] = 0.0f;
+        __syncwarp();
     }
 }
 
+// Blocks of a training call, each with a part in the workspace: four to an SM of 152.
+constexpr int kTrainBlocks = 608;
+
 int route_blocks(int64_t tokens) {
     const int64_t want = (tokens + kWarps - 1) / kWarps;
-    return static_cast<int>(want < 304 ? want : 304);
+    return static_cast<int>(want < kTrainBlocks ? want : kTrainBlocks);
 }
 
 bool sizes_ok(int64_t tokens, int experts, int topk) {
@@ -365,9 +452,16 @@ ep_status ep_route_backward(int64_t tokens, int32_t experts, int32_t topk, const
     p.topk_idx = topk_idx, p.topk_weights = topk_weights, p.lse = lse, p.slope = slope;
     p.dweights = dweights, p.dloss = dloss;
     p.experts = experts, p.topk = topk, p.renormalize = renormalize;
-    const unsigned grid = static_cast<unsigned>((tokens + kWarps - 1) / kWarps);
+    const int sms = sm_count_of(c.device);
+    if (sms < 1) return EP_ERR_CUDA;
+    const int64_t blocks = (tokens + kWarps - 1) / kWarps;
+    const unsigned grid = static_cast<unsigned>(blocks < 8 * sms ? blocks : 8 * sms);
     by_width(experts, [&](auto v) {
-        route_grad_kernel<decltype(v)::value><<<grid, 32 * kWarps, 0, static_cast<cudaStream_t>(stream)>>>(p);
+        auto kernel = route_grad_kernel<decltype(v)::value>;
+        const size_t smem = sizeof(float) * experts * kWarps;
+        if (smem > 48 * 1024)
+            (void)cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+        kernel<<<grid, 32 * kWarps, smem, static_cast<cudaStream_t>(stream)>>>(p);
     });
     return launched();
 }
