@@ -119,7 +119,7 @@ struct NormGradParams {
 // (rows team, team + teams, ...) and writes them once; dweight_kernel adds the
 // teams' sums in order.  All three rows are asked for before anything waits.
 template <int VPT, bool kWide>
-__global__ void __launch_bounds__(kWide ? 1024 : 32 * kTeams, kWide ? 1 : 3) norm_grad_kernel(NormGradParams p) {
+__global__ void __launch_bounds__(kWide ? 1024 : 32 * kTeams, kWide ? 1 : 4) norm_grad_kernel(NormGradParams p) {
     __shared__ float part[2][32];
     const int64_t team = kWide ? blockIdx.x : static_cast<int64_t>(blockIdx.x) * kTeams + (threadIdx.x >> 5);
     const int64_t teams = kWide ? gridDim.x : static_cast<int64_t>(gridDim.x) * kTeams;
@@ -221,11 +221,11 @@ struct Shape {
     int rows_per_block() const { return wide ? 1 : kTeams; }
 };
 
-// Blocks of the backward kernel: as many as run at once (24 warps an SM), so
+// Blocks of the backward kernel: as many as run at once (32 warps an SM), so
 // that a team keeps its sums over as many rows as it can.
 int grad_blocks(int64_t tokens, int hidden, int sms) {
     const Shape s(hidden, 2);
-    const int per_sm = s.warps >= 24 ? 1 : 24 / s.warps;
+    const int per_sm = 32 / s.warps;
     const int64_t rows = (tokens + s.rows_per_block() - 1) / s.rows_per_block();
     return static_cast<int>(rows < static_cast<int64_t>(sms) * per_sm ? rows : static_cast<int64_t>(sms) * per_sm);
 }

@@ -2,8 +2,9 @@
 // their weights, per-expert counts and the balance loss, and the logits'
 // gradient (include/ep_ops.h).
 //
-// A warp holds a token's logits in registers, VPT to a lane, expert
-// j * 32 + lane in step j.  Its K largest are found without sorting:
+// A warp holds a token's logits in registers, VPT to a lane, in vectors of V
+// neighbouring experts (V = 1 where a row's address or E does not allow more).
+// The K largest are found without sorting:
 //  - each lane's largest logit is known, and the K-th largest of these 32 (K
 //    warp-wide maxima) is a bound that at least K logits reach;
 //  - the few logits that reach it -- about K + 2 of 256 -- are written to
@@ -52,22 +53,50 @@ __device__ __forceinline__ unsigned long long pick_word(float l, int e) {
     return (static_cast<unsigned long long>(order_key(l)) << 32) | static_cast<uint32_t>(~e);
 }
 
-// Loads a lane's logits; what lies past the experts is -inf.
-template <int VPT>
+// The expert of a lane's j-th logit.
+template <int V>
+__device__ __forceinline__ int expert_of(int j, int lane) {
+    return (j / V) * 32 * V + lane * V + j % V;
+}
+
+// Loads a lane's logits; what lies past the experts is -inf.  For V > 1 the
+// experts and the row's address are multiples of V.
+template <int VPT, int V>
 __device__ __forceinline__ void load_row(const void *logits, int bf16, int64_t at, int experts, int lane, float (&l)[VPT]) {
-    if (bf16) {
-        const __nv_bfloat16 *row = static_cast<const __nv_bfloat16 *>(logits) + at;
 #pragma unroll
-        for (int j = 0; j < VPT; ++j) l[j] = j * 32 + lane < experts ? __bfloat162float(row[j * 32 + lane]) : -INFINITY;
-    } else {
-        const float *row = static_cast<const float *>(logits) + at;
+    for (int j = 0; j < VPT; j += V) {
+        const int e = expert_of<V>(j, lane);
+        if (e >= experts) {
 #pragma unroll
-        for (int j = 0; j < VPT; ++j) l[j] = j * 32 + lane < experts ? row[j * 32 + lane] : -INFINITY;
+            for (int i = 0; i < V; ++i) l[j + i] = -INFINITY;
+        } else if (bf16) {
+            const __nv_bfloat16 *from = static_cast<const __nv_bfloat16 *>(logits) + at + e;
+            if constexpr (V == 4) {
+                const uint2 u = *reinterpret_cast<const uint2 *>(from);
+                unpack2(u.x, l[j], l[j + 1]);
+                unpack2(u.y, l[j + 2], l[j + 3]);
+            } else if constexpr (V == 2) {
+                unpack2(*reinterpret_cast<const uint32_t *>(from), l[j], l[j + 1]);
+            } else {
+                l[j] = __bfloat162float(*from);
+            }
+        } else {
+            const float *from = static_cast<const float *>(logits) + at + e;
+            if constexpr (V == 4) {
+                const float4 u = *reinterpret_cast<const float4 *>(from);
+                l[j] = u.x, l[j + 1] = u.y, l[j + 2] = u.z, l[j + 3] = u.w;
+            } else if constexpr (V == 2) {
+                const float2 u = *reinterpret_cast<const float2 *>(from);
+                l[j] = u.x, l[j + 1] = u.y;
+            } else {
+                l[j] = *from;
+            }
+        }
     }
 }
 
 // Lane k gets pick k's word, 0 where there is none; `top`: the largest key.
-template <int VPT>
+template <int VPT, int V>
 __device__ __forceinline__ unsigned long long pick(const float (&l)[VPT], int K, int lane, unsigned long long *words,
                                                    unsigned long long *picks, uint32_t &top) {
     float most = l[0];
@@ -88,18 +117,25 @@ __device__ __forceinline__ unsigned long long pick(const float (&l)[VPT], int K,
         const bool on = l[j] >= least;
         const uint32_t lanes = __ballot_sync(0xffffffffu, on);
         const int at = n + __popc(lanes & ((1u << lane) - 1u));
-        if (on && at < kWords) words[at] = pick_word(l[j], j * 32 + lane);
+        if (on && at < kWords) words[at] = pick_word(l[j], expert_of<V>(j, lane));
         n += __popc(lanes);
     }
+    if (lane < 4 && n <= kWords) words[n + lane] = 0;
     __syncwarp();
     unsigned long long mine = 0;
     if (n <= kWords) {
         const unsigned long long a = lane < n ? words[lane] : 0, b = lane + 32 < n ? words[lane + 32] : 0;
         int above_a = 0, above_b = 0;
-        for (int q = 0; q < n; ++q) {
-            const unsigned long long w = words[q];
-            above_a += w > a;
-            above_b += w > b;
+        for (int q = 0; q < n; q += 4) {         // the list ends in four zeros
+            unsigned long long w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] = words[q + i];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) above_a += w[i] > a;
+            if (n > 32) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) above_b += w[i] > b;
+            }
         }
         if (a && above_a < K) picks[above_a] = a;
         if (b && above_b < K) picks[above_b] = b;
@@ -113,7 +149,7 @@ __device__ __forceinline__ unsigned long long pick(const float (&l)[VPT], int K,
             unsigned long long best = 0;
 #pragma unroll
             for (int j = 0; j < VPT; ++j) {
-                const unsigned long long w = l[j] > -INFINITY ? pick_word(l[j], j * 32 + lane) : 0;
+                const unsigned long long w = l[j] > -INFINITY ? pick_word(l[j], expert_of<V>(j, lane)) : 0;
                 if (w < last && w > best) best = w;
             }
 #pragma unroll
@@ -129,10 +165,10 @@ __device__ __forceinline__ unsigned long long pick(const float (&l)[VPT], int K,
     return mine;
 }
 
-template <int VPT, bool kTrain>
+template <int VPT, int V, bool kTrain>
 __global__ void __launch_bounds__(32 * kWarps) route_kernel(RouteParams p) {
     extern __shared__ float smem[];      // kTrain: p sums [kWarps][experts], then counts [experts]
-    __shared__ unsigned long long s_words[kWarps][kWords], s_picks[kWarps][kMaxTopk];
+    __shared__ unsigned long long s_words[kWarps][kWords + 4], s_picks[kWarps][kMaxTopk];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int E = p.experts, K = p.topk;
     int32_t *count = reinterpret_cast<int32_t *>(smem + (kTrain ? kWarps * E : 0));
@@ -144,14 +180,34 @@ __global__ void __launch_bounds__(32 * kWarps) route_kernel(RouteParams p) {
         for (int j = 0; j < VPT; ++j) psum[j] = 0.0f;
         __syncthreads();
     }
-    for (int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + warp; t < p.tokens;
-         t += static_cast<int64_t>(gridDim.x) * kWarps) {
-        const bool live = p.mask == nullptr || p.mask[t] != 0;
-        live_tokens += live;
+    const int64_t stride = static_cast<int64_t>(gridDim.x) * kWarps;
+    int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
+    // a token's logits are on their way while the last one's are worked on, where they fit twice
+    constexpr bool kAhead = VPT <= 16;
+    float ahead[kAhead ? VPT : 1];
+    bool live_ahead = false;
+    if (kAhead && t < p.tokens) {
+        live_ahead = p.mask == nullptr || p.mask[t] != 0;
+        if constexpr (kAhead) load_row<VPT, V>(p.logits, p.bf16, t * p.logits_stride, live_ahead ? E : 0, lane, ahead);
+    }
+    for (; t < p.tokens; t += stride) {
         float l[VPT];
-        load_row(p.logits, p.bf16, t * p.logits_stride, live ? E : 0, lane, l);
+        bool live;
+        if constexpr (kAhead) {
+            live = live_ahead;
+#pragma unroll
+            for (int j = 0; j < VPT; ++j) l[j] = ahead[j];
+            if (t + stride < p.tokens) {
+                live_ahead = p.mask == nullptr || p.mask[t + stride] != 0;
+                load_row<VPT, V>(p.logits, p.bf16, (t + stride) * p.logits_stride, live_ahead ? E : 0, lane, ahead);
+            }
+        } else {
+            live = p.mask == nullptr || p.mask[t] != 0;
+            load_row<VPT, V>(p.logits, p.bf16, t * p.logits_stride, live ? E : 0, lane, l);
+        }
+        live_tokens += live;
         uint32_t top;
-        const unsigned long long word = pick(l, K, lane, s_words[warp], s_picks[warp], top);
+        const unsigned long long word = pick<VPT, V>(l, K, lane, s_words[warp], s_picks[warp], top);
         const int my_e = word ? static_cast<int>(~static_cast<uint32_t>(word)) : -1;
         const float most = top ? key_value(top) : 0.0f;
         float sum = 0.0f;
@@ -186,7 +242,7 @@ __global__ void __launch_bounds__(32 * kWarps) route_kernel(RouteParams p) {
     if (kTrain) {
 #pragma unroll
         for (int j = 0; j < VPT; ++j)
-            if (j * 32 + lane < E) smem[warp * E + j * 32 + lane] = psum[j];
+            if (expert_of<V>(j, lane) < E) smem[warp * E + expert_of<V>(j, lane)] = psum[j];
         __shared__ int live_of[kWarps];
         if (lane == 0) live_of[warp] = live_tokens;
         __syncthreads();
@@ -269,7 +325,7 @@ struct RouteGradParams {
 // picked logits alone: a pick's logit gets w (dw - <w, dw>).  Otherwise a
 // weight is its p, and dw joins g.
 // The picks' parts go through a row of shared memory that is zero between tokens.
-template <int VPT>
+template <int VPT, int V>
 __global__ void __launch_bounds__(32 * kWarps) route_grad_kernel(RouteGradParams p) {
     extern __shared__ float smem[];      // [kWarps][experts]
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -282,14 +338,15 @@ __global__ void __launch_bounds__(32 * kWarps) route_grad_kernel(RouteGradParams
     float slope[kHeld ? VPT : 1];
     if (kHeld) {
 #pragma unroll
-        for (int j = 0; j < VPT; ++j) slope[j] = p.dloss && j * 32 + lane < E ? dloss * p.slope[j * 32 + lane] : 0.0f;
+        for (int j = 0; j < VPT; ++j)
+            slope[j] = p.dloss && expert_of<V>(j, lane) < E ? dloss * p.slope[expert_of<V>(j, lane)] : 0.0f;
     }
     for (int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + warp; t < p.tokens;
          t += static_cast<int64_t>(gridDim.x) * kWarps) {
         const float lse = p.lse[t];
         const bool live = !isinf(lse);       // +inf: a padded token, -inf: no logit left; both have p = 0
         float l[VPT];
-        load_row(p.logits, p.bf16, t * p.logits_stride, live ? E : 0, lane, l);
+        load_row<VPT, V>(p.logits, p.bf16, t * p.logits_stride, live ? E : 0, lane, l);
         int idx = -1;
         float w = 0.0f, add = 0.0f;
         if (lane < K) {
@@ -305,7 +362,7 @@ __global__ void __launch_bounds__(32 * kWarps) route_grad_kernel(RouteGradParams
         float g[VPT], inner = 0.0f;
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
-            const int e = j * 32 + lane;
+            const int e = expert_of<V>(j, lane);
             l[j] = live ? __expf(l[j] - lse) : 0.0f;
             g[j] = kHeld ? slope[j] : p.dloss && e < E ? dloss * p.slope[e] : 0.0f;
             if (!p.renormalize && e < E) g[j] += picks[e];
@@ -313,14 +370,23 @@ __global__ void __launch_bounds__(32 * kWarps) route_grad_kernel(RouteGradParams
         }
         inner = warp_sum(inner);
 #pragma unroll
-        for (int j = 0; j < VPT; ++j) {
-            const int e = j * 32 + lane;
+        for (int j = 0; j < VPT; j += V) {
+            const int e = expert_of<V>(j, lane);
             if (e < E) {
-                const float d = l[j] * (g[j] - inner) + (p.renormalize ? picks[e] : 0.0f);
-                if (p.bf16)
-                    static_cast<__nv_bfloat16 *>(p.dlogits)[t * p.dlogits_stride + e] = __float2bfloat16(d);
-                else
-                    static_cast<float *>(p.dlogits)[t * p.dlogits_stride + e] = d;
+                float d[V];
+#pragma unroll
+                for (int i = 0; i < V; ++i) d[i] = l[j + i] * (g[j + i] - inner) + (p.renormalize ? picks[e + i] : 0.0f);
+                if (p.bf16) {
+                    __nv_bfloat16 *to = static_cast<__nv_bfloat16 *>(p.dlogits) + t * p.dlogits_stride + e;
+                    if constexpr (V == 4) *reinterpret_cast<uint2 *>(to) = make_uint2(pack2(d[0], d[1]), pack2(d[2], d[3]));
+                    else if constexpr (V == 2) *reinterpret_cast<uint32_t *>(to) = pack2(d[0], d[1]);
+                    else *to = __float2bfloat16(d[0]);
+                } else {
+                    float *to = static_cast<float *>(p.dlogits) + t * p.dlogits_stride + e;
+                    if constexpr (V == 4) *reinterpret_cast<float4 *>(to) = make_float4(d[0], d[1], d[2], d[3]);
+                    else if constexpr (V == 2) *reinterpret_cast<float2 *>(to) = make_float2(d[0], d[1]);
+                    else *to = d[0];
+                }
             }
         }
         __syncwarp();
@@ -346,30 +412,35 @@ bool logits_ok(const void *p, int dtype, int64_t stride, int experts) {
            aligned(p, dtype == EP_DTYPE_F32 ? 4 : 2);
 }
 
-template <int VPT>
-void launch_route(const RouteParams &p, bool train, int grid, cudaStream_t st) {
-    const size_t smem = train ? sizeof(float) * p.experts * (kWarps + 1) : 0;
-    if (train) {
-        if (smem > 48 * 1024)
-            (void)cudaFuncSetAttribute(route_kernel<VPT, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(smem));
-        route_kernel<VPT, true><<<grid, 32 * kWarps, smem, st>>>(p);
-    } else {
-        route_kernel<VPT, false><<<grid, 32 * kWarps, smem, st>>>(p);
-    }
+// Dynamic shared memory of a kernel, asked for where it is more than is given without asking.
+template <typename K>
+void allow_smem(K kernel, size_t bytes) {
+    if (bytes > 48 * 1024)
+        (void)cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
 }
 
-// Calls f with the number of logits a lane holds, as a type.
-template <typename F>
-void by_width(int experts, F f) {
+// Whether rows of logits can be taken V at a time.
+bool by_vector(const void *p, int64_t stride, int experts, int bf16, int v) {
+    return experts % v == 0 && stride % v == 0 && aligned(p, static_cast<uintptr_t>(v * (bf16 ? 2 : 4)));
+}
+
+// Calls f with the number of logits a lane holds and the vector's length, as
+// types; can(V): whether vectors of V are allowed.
+template <int VPT, int V, typename C, typename F>
+void with_vector(C can, F f) {
+    if (can(V)) f(std::integral_constant<int, VPT>(), std::integral_constant<int, V>());
+    else f(std::integral_constant<int, VPT>(), std::integral_constant<int, 1>());
+}
+template <typename C, typename F>
+void by_width(int experts, C can, F f) {
     const int v = (experts + 31) / 32;
-    if (v <= 1) f(std::integral_constant<int, 1>());
-    else if (v <= 2) f(std::integral_constant<int, 2>());
-    else if (v <= 4) f(std::integral_constant<int, 4>());
-    else if (v <= 8) f(std::integral_constant<int, 8>());
-    else if (v <= 16) f(std::integral_constant<int, 16>());
-    else if (v <= 32) f(std::integral_constant<int, 32>());
-    else f(std::integral_constant<int, 128>());
+    if (v <= 1) f(std::integral_constant<int, 1>(), std::integral_constant<int, 1>());
+    else if (v <= 2) with_vector<2, 2>(can, f);
+    else if (v <= 4) with_vector<4, 4>(can, f);
+    else if (v <= 8) with_vector<8, 4>(can, f);
+    else if (v <= 16) with_vector<16, 4>(can, f);
+    else if (v <= 32) with_vector<32, 4>(can, f);
+    else f(std::integral_constant<int, 128>(), std::integral_constant<int, 1>());
 }
 
 }  // namespace
@@ -421,8 +492,21 @@ ep_status ep_route(int64_t tokens, int32_t experts, int32_t topk, const void *lo
         p.part_live = p.part_count + static_cast<int64_t>(blocks) * experts;
     }
     if (tokens > 0) {
-        const int grid = train ? blocks : static_cast<int>((tokens + kWarps - 1) / kWarps);
-        by_width(experts, [&](auto v) { launch_route<decltype(v)::value>(p, train, grid, st); });
+        const int sms = sm_count_of(c.device);
+        if (sms < 1) return EP_ERR_CUDA;
+        const int64_t most = (tokens + kWarps - 1) / kWarps;
+        const int grid = train ? blocks : static_cast<int>(most < 4 * sms ? most : 4 * sms);
+        const size_t smem = train ? sizeof(float) * experts * (kWarps + 1) : 0;
+        by_width(experts, [&](int v) { return by_vector(logits, logits_stride, experts, p.bf16, v); },
+                 [&](auto vpt, auto v) {
+                     constexpr int VPT = decltype(vpt)::value, V = decltype(v)::value;
+                     if (train) {
+                         allow_smem(route_kernel<VPT, V, true>, smem);
+                         route_kernel<VPT, V, true><<<grid, 32 * kWarps, smem, st>>>(p);
+                     } else {
+                         route_kernel<VPT, V, false><<<grid, 32 * kWarps, 0, st>>>(p);
+                     }
+                 });
     }
     if (train)
         balance_kernel<<<1, 1024, 0, st>>>(p.part_p, p.part_count, p.part_live, tokens > 0 ? blocks : 0, experts,
@@ -456,13 +540,17 @@ ep_status ep_route_backward(int64_t tokens, int32_t experts, int32_t topk, const
     if (sms < 1) return EP_ERR_CUDA;
     const int64_t blocks = (tokens + kWarps - 1) / kWarps;
     const unsigned grid = static_cast<unsigned>(blocks < 8 * sms ? blocks : 8 * sms);
-    by_width(experts, [&](auto v) {
-        auto kernel = route_grad_kernel<decltype(v)::value>;
-        const size_t smem = sizeof(float) * experts * kWarps;
-        if (smem > 48 * 1024)
-            (void)cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-        kernel<<<grid, 32 * kWarps, smem, static_cast<cudaStream_t>(stream)>>>(p);
-    });
+    const size_t smem = sizeof(float) * experts * kWarps;
+    by_width(experts,
+             [&](int v) {
+                 return by_vector(logits, logits_stride, experts, p.bf16, v) &&
+                        by_vector(dlogits, dlogits_stride, experts, p.bf16, v);
+             },
+             [&](auto vpt, auto v) {
+                 auto kernel = route_grad_kernel<decltype(vpt)::value, decltype(v)::value>;
+                 allow_smem(kernel, smem);
+                 kernel<<<grid, 32 * kWarps, smem, static_cast<cudaStream_t>(stream)>>>(p);
+             });
     return launched();
 }
 
