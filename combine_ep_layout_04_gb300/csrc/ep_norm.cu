@@ -41,64 +41,68 @@ __device__ __forceinline__ float team_sum(float v, float *smem) {
     return warp_sum((threadIdx.x & 31) < warps ? smem[threadIdx.x & 31] : 0.0f);
 }
 
-template <int VPT, bool kWide>
-__global__ void __launch_bounds__(kWide ? 1024 : 32 * kTeams) norm_kernel(NormParams p) {
+// kFull: the lanes' vectors are the row's, none past its end.
+template <int VPT, bool kWide, bool kFull>
+__global__ void __launch_bounds__(kWide ? 1024 : 32 * kTeams) norm_kernel(const __grid_constant__ NormParams p) {
     __shared__ float part[32];
     const int64_t t = kWide ? blockIdx.x : static_cast<int64_t>(blockIdx.x) * kTeams + (threadIdx.x >> 5);
     if (t >= p.tokens) return;
     const int lane = kWide ? threadIdx.x : threadIdx.x & 31;
     const int width = kWide ? blockDim.x : 32;
     const int nvec = p.hidden >> 3;
+    const uint4 *x = reinterpret_cast<const uint4 *>(p.x + t * p.x_stride) + lane;
+    const uint4 *res = reinterpret_cast<const uint4 *>(p.residual + t * p.residual_stride) + lane;
+    uint4 a[VPT], b[VPT];
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+        a[i] = b[i] = make_uint4(0, 0, 0, 0);
+        if (kFull || i * width + lane < nvec) {
+            a[i] = x[i * width];
+            if (p.residual) b[i] = res[i * width];
+        }
+    }
     float h[VPT][8];
     float sum = 0.0f;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-        const int v = i * width + lane;
+        float r[8];
+        unpack8(a[i], h[i]);
+        unpack8(b[i], r);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) h[i][j] = 0.0f;
-        if (v < nvec) {
-            unpack8(*reinterpret_cast<const uint4 *>(p.x + t * p.x_stride + v * 8), h[i]);
-            if (p.residual) {
-                float r[8];
-                unpack8(*reinterpret_cast<const uint4 *>(p.residual + t * p.residual_stride + v * 8), r);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) h[i][j] += r[j];
-            }
+        for (int j = 0; j < 8; ++j) {
+            h[i][j] += r[j];
+            sum = fmaf(h[i][j], h[i][j], sum);
         }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) sum = fmaf(h[i][j], h[i][j], sum);
     }
     sum = team_sum<kWide>(sum, part);
     const float rstd = 1.0f / sqrtf(sum / static_cast<float>(p.hidden) + p.eps);
     if (p.rstd && lane == 0) p.rstd[t] = rstd;
+    uint4 *stream = reinterpret_cast<uint4 *>(p.residual_out + t * p.residual_out_stride) + lane;
+    uint4 *out = reinterpret_cast<uint4 *>(p.out + t * p.out_stride) + lane;
+    uint2 *values = reinterpret_cast<uint2 *>(p.values + t * p.value_stride) + lane;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-        const int v = i * width + lane;
-        if (v < nvec && p.residual_out)
-            *reinterpret_cast<uint4 *>(p.residual_out + t * p.residual_out_stride + v * 8) = pack8(h[i]);
-        float y[8];
+        const bool there = kFull || i * width + lane < nvec;
+        if (p.residual_out && there) stream[i * width] = pack8(h[i]);
+        float w[8];
+        if (there) {
+            load8(p.weight, p.weight_dtype, (i * width + lane) * 8, w);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) y[j] = 0.0f;
-        if (v < nvec) {
-            float w[8];
-            load8(p.weight, p.weight_dtype, v * 8, w);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) y[j] = h[i][j] * rstd * w[j];
-            if (p.out) *reinterpret_cast<uint4 *>(p.out + t * p.out_stride + v * 8) = pack8(y);
+            for (int j = 0; j < 8; ++j) h[i][j] = h[i][j] * rstd * w[j];
+            if (p.out) out[i * width] = pack8(h[i]);
         }
         if (p.values) {
             // a block of 128 columns is 16 neighbouring lanes (the lanes past the row hold zeros)
             float m = kFloor;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) m = max_nan(m, fabsf(y[j]));
+            for (int j = 0; j < 8; ++j) m = max_nan(m, fabsf(h[i][j]));
 #pragma unroll
             for (int o = 8; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
-            if (v < nvec) {
+            if (there) {
                 const float inv = kFp8Max / m;
-                if ((v & 15) == 0) p.scales[t * p.scale_stride + (v >> 4)] = m * (1.0f / kFp8Max);
-                *reinterpret_cast<uint2 *>(p.values + t * p.value_stride + v * 8) =
-                    make_uint2(pack_fp8x4(y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv),
-                               pack_fp8x4(y[4] * inv, y[5] * inv, y[6] * inv, y[7] * inv));
+                if ((lane & 15) == 0) p.scales[t * p.scale_stride + ((i * width + lane) >> 4)] = m * (1.0f / kFp8Max);
+                values[i * width] = make_uint2(pack_fp8x4(h[i][0] * inv, h[i][1] * inv, h[i][2] * inv, h[i][3] * inv),
+                                               pack_fp8x4(h[i][4] * inv, h[i][5] * inv, h[i][6] * inv, h[i][7] * inv));
             }
         }
     }
@@ -273,14 +277,12 @@ ep_status ep_rms_norm(int64_t tokens, int32_t hidden, const void *x, int64_t x_s
     const Shape s(hidden, 4);
     const unsigned grid = static_cast<unsigned>((tokens + s.rows_per_block() - 1) / s.rows_per_block());
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (s.wide)
-        norm_kernel<4, true><<<grid, 32 * s.warps, 0, st>>>(p);
-    else if (s.vpt == 4)
-        norm_kernel<4, false><<<grid, 32 * kTeams, 0, st>>>(p);
-    else if (s.vpt == 2)
-        norm_kernel<2, false><<<grid, 32 * kTeams, 0, st>>>(p);
-    else
-        norm_kernel<1, false><<<grid, 32 * kTeams, 0, st>>>(p);
+    const bool full = hidden / 8 == s.vpt * (s.wide ? 32 * s.warps : 32);
+    auto launch = [&](auto kernel) { kernel<<<grid, 32 * s.warps, 0, st>>>(p); };
+    if (s.wide) launch(full ? norm_kernel<4, true, true> : norm_kernel<4, true, false>);
+    else if (s.vpt == 4) launch(full ? norm_kernel<4, false, true> : norm_kernel<4, false, false>);
+    else if (s.vpt == 2) launch(full ? norm_kernel<2, false, true> : norm_kernel<2, false, false>);
+    else launch(full ? norm_kernel<1, false, true> : norm_kernel<1, false, false>);
     return launched();
 }
 

@@ -34,6 +34,7 @@ struct RouteParams {
     float *part_p;                 // [grid, experts] sums of p over a block's tokens
     int32_t *part_count;           // [grid, experts] picks
     int32_t *part_live;            // [grid] tokens the mask keeps
+    unsigned int *done;            // zeroed for the kernel that adds the parts
     int experts, topk, renormalize, per_rank, bf16;
 };
 
@@ -111,14 +112,22 @@ __device__ __forceinline__ unsigned long long pick(const float (&l)[VPT], int K,
     }
     // fewer than K different maxima: every logit above -inf is on the list
     const float least = bound ? key_value(bound) : -3.402823466e38f;
+    // a lane's logits on the list, a bit each; lanes write one after another of theirs, most have none
     int n = 0;
 #pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-        const bool on = l[j] >= least;
-        const uint32_t lanes = __ballot_sync(0xffffffffu, on);
-        const int at = n + __popc(lanes & ((1u << lane) - 1u));
-        if (on && at < kWords) words[at] = pick_word(l[j], expert_of<V>(j, lane));
-        n += __popc(lanes);
+    for (int j0 = 0; j0 < VPT; j0 += 32) {
+        uint32_t on = 0;
+#pragma unroll
+        for (int j = j0; j < VPT && j < j0 + 32; ++j) on |= l[j] >= least ? 1u << (j - j0) : 0u;
+        for (uint32_t lanes = __ballot_sync(0xffffffffu, on != 0); lanes; lanes = __ballot_sync(0xffffffffu, on != 0)) {
+            const int j = __ffs(on) - 1, at = n + __popc(lanes & ((1u << lane) - 1u));
+            float v = l[j0];
+#pragma unroll
+            for (int i = j0 + 1; i < VPT && i < j0 + 32; ++i) v = i - j0 == j ? l[i] : v;
+            if (on && at < kWords) words[at] = pick_word(v, expert_of<V>(j0 + j, lane));
+            on &= on - 1;
+            n += __popc(lanes);
+        }
     }
     if (lane < 4 && n <= kWords) words[n + lane] = 0;
     __syncwarp();
@@ -127,9 +136,9 @@ __device__ __forceinline__ unsigned long long pick(const float (&l)[VPT], int K,
         const unsigned long long a = lane < n ? words[lane] : 0, b = lane + 32 < n ? words[lane + 32] : 0;
         int above_a = 0, above_b = 0;
         for (int q = 0; q < n; q += 4) {         // the list ends in four zeros
-            unsigned long long w[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) w[i] = words[q + i];
+            const ulonglong2 u = *reinterpret_cast<const ulonglong2 *>(words + q);
+            const ulonglong2 v = *reinterpret_cast<const ulonglong2 *>(words + q + 2);
+            const unsigned long long w[4] = {u.x, u.y, v.x, v.y};
 #pragma unroll
             for (int i = 0; i < 4; ++i) above_a += w[i] > a;
             if (n > 32) {
@@ -166,15 +175,16 @@ __device__ __forceinline__ unsigned long long pick(const float (&l)[VPT], int K,
 }
 
 template <int VPT, int V, bool kTrain>
-__global__ void __launch_bounds__(32 * kWarps) route_kernel(RouteParams p) {
+__global__ void __launch_bounds__(32 * kWarps, VPT <= 8 ? 4 : 1) route_kernel(RouteParams p) {
     extern __shared__ float smem[];      // kTrain: p sums [kWarps][experts], then counts [experts]
-    __shared__ unsigned long long s_words[kWarps][kWords + 4], s_picks[kWarps][kMaxTopk];
+    __shared__ __align__(16) unsigned long long s_words[kWarps][kWords + 4], s_picks[kWarps][kMaxTopk];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int E = p.experts, K = p.topk;
     int32_t *count = reinterpret_cast<int32_t *>(smem + (kTrain ? kWarps * E : 0));
     float psum[kTrain ? VPT : 1];
     int live_tokens = 0;
     if (kTrain) {
+        if (blockIdx.x == 0 && threadIdx.x == 0) *p.done = 0;
         for (int e = threadIdx.x; e < E; e += blockDim.x) count[e] = 0;
 #pragma unroll
         for (int j = 0; j < VPT; ++j) psum[j] = 0.0f;
@@ -221,7 +231,7 @@ __global__ void __launch_bounds__(32 * kWarps) route_kernel(RouteParams p) {
         }
         float w = word ? __expf(key_value(static_cast<uint32_t>(word >> 32)) - most) : 0.0f;
         const float total = p.renormalize ? warp_sum(w) : sum;
-        w = word ? w / total : 0.0f;
+        w = word ? __fdividef(w, total) : 0.0f;      // total is 1 .. experts, or NaN
         if (lane < K) {
             p.topk_idx[t * K + lane] = my_e;
             p.topk_weights[t * K + lane] = w;
@@ -260,54 +270,66 @@ __global__ void __launch_bounds__(32 * kWarps) route_kernel(RouteParams p) {
     }
 }
 
-// Adds the blocks' sums in order and makes counts, slope and loss; one block.
-// Up to 1024 / experts threads share an expert, each takes every so many
-// blocks, and their sums are added in order.
-__global__ void __launch_bounds__(1024) balance_kernel(const float *part_p, const int32_t *part_count,
-                                                       const int32_t *part_live, int parts, int experts, int topk,
-                                                       float coef, int32_t *expert_count, float *loss, float *slope) {
-    __shared__ float sums[32], s_p[1024];
-    __shared__ int s_live[32], s_n[1024];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+// Adds the blocks' sums in order and makes counts, slope and loss: 32 experts
+// to a block, 32 warps that take every 32nd of the routing blocks.  The last
+// block to finish adds the blocks' parts of the loss, in order too.
+struct BalanceParams {
+    const float *part_p;
+    const int32_t *part_count, *part_live;
+    float *part_loss;
+    unsigned int *done;
+    int parts, experts, topk;
+    float coef;
+    int32_t *expert_count;
+    float *loss, *slope;
+};
+
+__global__ void __launch_bounds__(1024) balance_kernel(BalanceParams p) {
+    __shared__ float s_p[32][33];
+    __shared__ int s_n[32][33], s_live[32];
+    __shared__ bool s_last;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, e = blockIdx.x * 32 + lane;
     int live = 0;
-    for (int b = tid; b < parts; b += 1024) live += part_live[b];
+    for (int b = tid; b < p.parts; b += 1024) live += p.part_live[b];
+    float s = 0.0f;
+    int n = 0;
+    if (e < p.experts) {
+#pragma unroll 8
+        for (int b = warp; b < p.parts; b += 32) {
+            s += p.part_p[static_cast<int64_t>(b) * p.experts + e];
+            n += p.part_count[static_cast<int64_t>(b) * p.experts + e];
+        }
+    }
+    s_p[warp][lane] = s;
+    s_n[warp][lane] = n;
     live = __reduce_add_sync(0xffffffffu, live);
     if (lane == 0) s_live[warp] = live;
     __syncthreads();
-    live = __reduce_add_sync(0xffffffffu, s_live[lane]);
-    const float tv = live > 0 ? static_cast<float>(live) : 1.0f;
-    const float scale = coef * static_cast<float>(experts) / (static_cast<float>(topk) * tv * tv);
-    const int share = experts < 1024 ? 1024 / experts : 1, span = experts < 1024 ? experts : 1024;
-    float sum = 0.0f;
-    for (int e0 = 0; e0 < experts; e0 += span) {
-        const int e = e0 + tid % span, g = tid / span;
-        float s = 0.0f;
-        int n = 0;
-        if (e < experts && g < share) {
-#pragma unroll 8
-            for (int b = g; b < parts; b += share) {
-                s += part_p[static_cast<int64_t>(b) * experts + e];
-                n += part_count[static_cast<int64_t>(b) * experts + e];
-            }
-        }
-        __syncthreads();
-        s_p[tid] = s;
-        s_n[tid] = n;
-        __syncthreads();
-        if (g == 0 && e < experts) {
-            for (int i = 1; i < share; ++i) s += s_p[i * span + tid], n += s_n[i * span + tid];
-            const float slope_e = scale * static_cast<float>(n);
-            expert_count[e] = n;
-            slope[e] = slope_e;
-            sum += slope_e * s;
-        }
-    }
-    sum = warp_sum(sum);
-    if (lane == 0) sums[warp] = sum;
-    __syncthreads();
     if (warp == 0) {
-        sum = warp_sum(sums[lane]);
-        if (lane == 0) *loss = sum;
+        live = __reduce_add_sync(0xffffffffu, s_live[lane]);
+        const float tv = live > 0 ? static_cast<float>(live) : 1.0f;
+        const float scale = p.coef * static_cast<float>(p.experts) / (static_cast<float>(p.topk) * tv * tv);
+        s = 0.0f;
+        n = 0;
+        for (int w = 0; w < 32; ++w) s += s_p[w][lane], n += s_n[w][lane];
+        const float g = scale * static_cast<float>(n);
+        if (e < p.experts) {
+            p.expert_count[e] = n;
+            p.slope[e] = g;
+        }
+        s = warp_sum(e < p.experts ? g * s : 0.0f);
+        if (lane == 0) {
+            p.part_loss[blockIdx.x] = s;
+            s_last = atom_add_acq_rel(p.done, 1u) == gridDim.x - 1;
+        }
+        __syncwarp();
+        if (s_last) {
+            s = 0.0f;
+            for (int b = lane; b < static_cast<int>(gridDim.x); b += 32)
+                s += *static_cast<volatile const float *>(p.part_loss + b);
+            s = warp_sum(s);
+            if (lane == 0) *p.loss = s;
+        }
     }
 }
 
@@ -326,7 +348,7 @@ struct RouteGradParams {
 // weight is its p, and dw joins g.
 // The picks' parts go through a row of shared memory that is zero between tokens.
 template <int VPT, int V>
-__global__ void __launch_bounds__(32 * kWarps) route_grad_kernel(RouteGradParams p) {
+__global__ void __launch_bounds__(32 * kWarps, VPT <= 8 ? 4 : 1) route_grad_kernel(RouteGradParams p) {
     extern __shared__ float smem[];      // [kWarps][experts]
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int E = p.experts, K = p.topk;
@@ -341,21 +363,32 @@ __global__ void __launch_bounds__(32 * kWarps) route_grad_kernel(RouteGradParams
         for (int j = 0; j < VPT; ++j)
             slope[j] = p.dloss && expert_of<V>(j, lane) < E ? dloss * p.slope[expert_of<V>(j, lane)] : 0.0f;
     }
-    for (int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + warp; t < p.tokens;
-         t += static_cast<int64_t>(gridDim.x) * kWarps) {
-        const float lse = p.lse[t];
-        const bool live = !isinf(lse);       // +inf: a padded token, -inf: no logit left; both have p = 0
-        float l[VPT];
-        load_row<VPT, V>(p.logits, p.bf16, t * p.logits_stride, live ? E : 0, lane, l);
-        int idx = -1;
-        float w = 0.0f, add = 0.0f;
+    const int64_t stride = static_cast<int64_t>(gridDim.x) * kWarps;
+    int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
+    // A token's inputs are on their way while the last one's are worked on.
+    // lse is +inf for a padded token and -inf where no logit was left: both
+    // have p = 0, whatever the logits hold.
+    float ahead[VPT], lse_ahead = 0.0f, w_ahead = 0.0f, add_ahead = 0.0f;
+    int idx_ahead = -1;
+    auto fetch = [&](int64_t at) {
+        lse_ahead = p.lse[at];
+        load_row<VPT, V>(p.logits, p.bf16, at * p.logits_stride, E, lane, ahead);
         if (lane < K) {
-            idx = p.topk_idx[t * K + lane];
-            if (idx >= 0) {
-                w = p.topk_weights[t * K + lane];
-                add = p.dweights[t * K + lane];
-            }
+            idx_ahead = p.topk_idx[at * K + lane];
+            w_ahead = p.topk_weights[at * K + lane];
+            add_ahead = p.dweights[at * K + lane];
         }
+    };
+    if (t < p.tokens) fetch(t);
+    for (; t < p.tokens; t += stride) {
+        const float lse = lse_ahead;
+        const bool live = !isinf(lse);
+        float l[VPT];
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) l[j] = ahead[j];
+        const int idx = idx_ahead;
+        float w = idx >= 0 ? w_ahead : 0.0f, add = idx >= 0 ? add_ahead : 0.0f;
+        if (t + stride < p.tokens) fetch(t + stride);
         if (p.renormalize) add = w * (add - warp_sum(w * add));
         if (idx >= 0 && idx < E) picks[idx] = add;
         __syncwarp();
@@ -402,6 +435,8 @@ int route_blocks(int64_t tokens) {
     const int64_t want = (tokens + kWarps - 1) / kWarps;
     return static_cast<int>(want < kTrainBlocks ? want : kTrainBlocks);
 }
+
+int balance_blocks(int experts) { return (experts + 31) / 32; }
 
 bool sizes_ok(int64_t tokens, int experts, int topk) {
     return tokens >= 0 && tokens < (1ll << 31) && experts >= 1 && experts <= kMaxExperts && topk >= 1 &&
@@ -450,7 +485,7 @@ extern "C" {
 int64_t ep_route_workspace(int64_t tokens, int32_t experts) {
     if (!sizes_ok(tokens, experts, 1)) return 0;
     const int64_t blocks = route_blocks(tokens);
-    return (blocks * (2 * static_cast<int64_t>(experts) + 1)) * 4 + 16;
+    return (blocks * (2 * static_cast<int64_t>(experts) + 1) + balance_blocks(experts) + 1) * 4 + 16;
 }
 
 ep_status ep_route(int64_t tokens, int32_t experts, int32_t topk, const void *logits, int32_t logits_dtype,
@@ -490,6 +525,7 @@ ep_status ep_route(int64_t tokens, int32_t experts, int32_t topk, const void *lo
         p.part_p = static_cast<float *>(workspace);
         p.part_count = reinterpret_cast<int32_t *>(p.part_p + static_cast<int64_t>(blocks) * experts);
         p.part_live = p.part_count + static_cast<int64_t>(blocks) * experts;
+        p.done = reinterpret_cast<unsigned int *>(p.part_live + blocks);
     }
     if (tokens > 0) {
         const int sms = sm_count_of(c.device);
@@ -508,9 +544,15 @@ ep_status ep_route(int64_t tokens, int32_t experts, int32_t topk, const void *lo
                      }
                  });
     }
-    if (train)
-        balance_kernel<<<1, 1024, 0, st>>>(p.part_p, p.part_count, p.part_live, tokens > 0 ? blocks : 0, experts,
-                                           topk, coef, expert_count, loss, slope);
+    if (train) {
+        if (tokens == 0 && cudaMemsetAsync(p.done, 0, sizeof(unsigned int), st) != cudaSuccess) return EP_ERR_CUDA;
+        BalanceParams b{};
+        b.part_p = p.part_p, b.part_count = p.part_count, b.part_live = p.part_live;
+        b.done = p.done, b.part_loss = reinterpret_cast<float *>(p.done + 1);
+        b.parts = tokens > 0 ? blocks : 0, b.experts = experts, b.topk = topk, b.coef = coef;
+        b.expert_count = expert_count, b.loss = loss, b.slope = slope;
+        balance_kernel<<<balance_blocks(experts), 1024, 0, st>>>(b);
+    }
     return launched();
 }
 
