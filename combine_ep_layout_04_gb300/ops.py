@@ -35,15 +35,16 @@ def _blocks(n: int) -> int:
     return (n + BLOCK - 1) // BLOCK
 
 
-@dataclasses.dataclass
 class Fp8Rows:
     """8-bit rows: `values` float8_e4m3fn [rows, width] and `scales` fp32
     [rows, ceil(width / 128)]; a value stands for value * scale of its block.
     Columns are dense, rows may be strided.  Rows made by empty() lie in one
     buffer each (the values, then the scales, padded to 16 bytes), so that
     `packed` -- the same memory as bf16 -- can be dispatched."""
-    values: torch.Tensor
-    scales: torch.Tensor
+    __slots__ = ("_values", "_scales", "_buffer", "_width")
+
+    def __init__(self, values: torch.Tensor, scales: torch.Tensor):
+        self._values, self._scales, self._buffer, self._width = values, scales, None, 0
 
     @staticmethod
     def packed_width(width: int) -> int:
@@ -55,7 +56,7 @@ class Fp8Rows:
         if width < 8 or width % 8:
             raise ValueError(f"width: {width}, expected a multiple of 8")
         device = torch.device("cuda", torch.cuda.current_device()) if device is None else device
-        return cls.from_packed(torch.empty((rows, cls.packed_width(width)), dtype=_BF16, device=device), width)
+        return cls._in(torch.empty((rows, 2 * cls.packed_width(width)), dtype=_FP8, device=device), width)
 
     @classmethod
     def from_packed(cls, rows: torch.Tensor, width: int) -> "Fp8Rows":
@@ -64,26 +65,46 @@ class Fp8Rows:
             raise TypeError(f"rows: expected a torch.Tensor, got {type(rows).__name__}")
         if rows.dtype != _BF16:
             raise TypeError(f"rows: dtype {rows.dtype}, expected {_BF16}")
+        if width < 8 or width % 8:
+            raise ValueError(f"width: {width}, expected a multiple of 8")
         if rows.dim() != 2 or rows.shape[1] != cls.packed_width(width) or not rows.is_contiguous():
             raise ValueError(f"rows: expected contiguous [*, {cls.packed_width(width)}], got {tuple(rows.shape)}")
-        at = _scales_at(width)
-        self = cls(rows.view(_FP8)[:, :width], rows.view(_F32)[:, at // 4:at // 4 + _blocks(width)])
-        self._packed = rows
+        return cls._in(rows.view(_FP8), width)
+
+    @classmethod
+    def _in(cls, buffer: torch.Tensor, width: int) -> "Fp8Rows":
+        self = cls(None, None)
+        self._buffer, self._width = buffer, width
         return self
 
     @property
+    def values(self) -> torch.Tensor:
+        if self._values is None:
+            self._values = self._buffer.narrow(1, 0, self._width)
+        return self._values
+
+    @property
+    def scales(self) -> torch.Tensor:
+        if self._scales is None:
+            self._scales = self._buffer.view(_F32).narrow(1, _scales_at(self._width) // 4, _blocks(self._width))
+        return self._scales
+
+    @property
     def packed(self) -> torch.Tensor:
-        rows = getattr(self, "_packed", None)
-        if rows is None:
+        if self._buffer is None:
             raise ValueError("these rows do not lie in packed form (use Fp8Rows.empty or from_packed)")
-        return rows
+        return self._buffer.view(_BF16)
 
     def float(self) -> torch.Tensor:
         """What the rows stand for, in fp32 (for inspection; no kernel of this library)."""
         return self.values.float() * self.scales.repeat_interleave(BLOCK, 1)[:, :self.values.shape[1]]
 
+    def __repr__(self) -> str:
+        return f"Fp8Rows({self.values.shape[0]} x {self.values.shape[1]}, {self.values.device})"
+
 
 def _scales_at(width: int) -> int:
+    """Bytes from a packed row's start to its scales."""
     return (width + 3) // 4 * 4
 
 
@@ -110,32 +131,43 @@ class Routing:
     renormalize: bool
 
 
-def _check(t, name: str, dtype, device, shape) -> None:
+# A call's checks cost as much as a small call's kernel, so each tensor is first
+# compared with what it should be in one go; only one that differs is looked at
+# again to say how (or, for rows, to see whether it will do after all).
+
+def _check(t, name: str, dtype, index: int, shape) -> None:
     """Raise unless t is a tensor of `dtype` (one of them, if a tuple) and
-    `shape` (None matches any size) on `device`, with dense columns."""
+    `shape` (None matches any size) on CUDA device `index`."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
     if t.dtype != dtype and not (isinstance(dtype, tuple) and t.dtype in dtype):
         raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
-    if t.device != device:
-        raise ValueError(f"{name}: on {t.device}, expected {device}")
+    if t.get_device() != index:
+        raise ValueError(f"{name}: on {t.device}, expected cuda:{index}")
     got = t.shape
     if len(got) != len(shape) or any(w is not None and g != w for g, w in zip(got, shape)):
         raise ValueError(f"{name}: shape {tuple(got)}, expected {tuple('*' if v is None else v for v in shape)}")
 
 
-def _dense(t, name: str, dtype, device, shape) -> int:
-    """_check of a contiguous tensor; its address."""
-    _check(t, name, dtype, device, shape)
-    if not t.is_contiguous():
+def _dense(t, name: str, dtype, index: int, shape) -> int:
+    """Address of a contiguous tensor of exactly this type, device and shape."""
+    if not (isinstance(t, torch.Tensor) and t.dtype == dtype and t.shape == shape and t.get_device() == index
+            and t.is_contiguous()):
+        _check(t, name, dtype, index, shape)
         raise ValueError(f"{name}: must be contiguous")
     return t.data_ptr()
 
 
-def _rows(t, name: str, dtype, device, shape, align: int) -> tuple[int, int]:
-    """_check of a matrix whose columns are dense and whose rows start on
-    multiples of `align` bytes; its address and row stride in elements."""
-    _check(t, name, dtype, device, shape)
+def _rows(t, name: str, dtype, index: int, shape, align: int) -> tuple[int, int]:
+    """Address and row stride in elements of a matrix of exactly this type,
+    device and shape whose columns are dense and whose rows start on multiples
+    of `align` bytes."""
+    if isinstance(t, torch.Tensor) and t.dtype == dtype and t.shape == shape and t.get_device() == index \
+            and t.is_contiguous():
+        ptr, width = t.data_ptr(), shape[1]
+        if not (ptr | width * dtype.itemsize) & (align - 1):
+            return ptr, width
+    _check(t, name, dtype, index, shape)
     n, width = t.shape
     stride = t.stride(0) if n > 1 else max(width, t.stride(0))
     size, ptr = t.element_size(), t.data_ptr()
@@ -151,27 +183,72 @@ def _rows(t, name: str, dtype, device, shape, align: int) -> tuple[int, int]:
     return ptr, stride
 
 
-def _device_of(t, name: str) -> torch.device:
+def _matrix(t, name: str, dtype, index: int) -> tuple[int, int]:
+    """Sizes of a matrix of this type (one of them, if a tuple) on the device."""
+    if not isinstance(t, torch.Tensor) or t.dim() != 2:
+        _check(t, name, dtype, index, (None, None))
+    return t.shape
+
+
+def _fp8_rows(r, name: str, index: int, shape, align: int) -> tuple[int, int, int, int]:
+    """Addresses and strides of 8-bit rows: values, scales."""
+    if not isinstance(r, Fp8Rows):
+        raise TypeError(f"{name}: expected Fp8Rows, got {type(r).__name__}")
+    buffer = r._buffer
+    if buffer is not None and r._width == shape[1] and buffer.shape[0] == shape[0] and buffer.get_device() == index:
+        ptr, stride = buffer.data_ptr(), buffer.shape[1]
+        if not ptr & 15:
+            return ptr, stride, ptr + _scales_at(shape[1]), stride // 4
+    pv, sv = _rows(r.values, name + ".values", _FP8, index, shape, align)
+    ps, ss = _rows(r.scales, name + ".scales", _F32, index, (shape[0], _blocks(shape[1])), 4)
+    return pv, sv, ps, ss
+
+
+def _device_of(t, name: str) -> tuple[torch.device, int]:
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
-    if not t.is_cuda:
+    index = t.get_device()
+    if index < 0:
         raise ValueError(f"{name}: on {t.device}, expected a CUDA device")
-    return t.device
+    return t.device, index
 
 
-def _call(device: torch.device, fn, *args) -> None:
-    """fn(*args, stream) on the current stream of `device`, made current for the call."""
-    stream = torch.cuda.current_stream(device).cuda_stream
-    if torch.cuda.current_device() == device.index:
-        fn(*args, stream)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _call(index: int, what: str, *args) -> None:
+    """Calls the library on the current stream of device `index`, made current for the call."""
+    if torch.cuda.current_device() == index:
+        status = getattr(_ep.lib, what)(*args, _raw_stream(index))
     else:
-        with torch.cuda.device(device):
-            fn(*args, stream)
+        with torch.cuda.device(index):
+            status = getattr(_ep.lib, what)(*args, _raw_stream(index))
+    if status != _ep.EP_OK:
+        raise _ep.EpError(status, what)
 
 
 def _check_hidden(h: int) -> None:
     if h < 8 or h % 8 or h > 32768:
         raise ValueError(f"hidden: {h}, expected a multiple of 8 up to 32768")
+
+
+def _weight(w, index: int, h: int) -> tuple[int, int]:
+    """Address and type of a norm's weight vector."""
+    dtype = _F32 if isinstance(w, torch.Tensor) and w.dtype == _F32 else _BF16
+    if not isinstance(w, torch.Tensor) or w.dtype != dtype:
+        _check(w, "weight", (_BF16, _F32), index, (h,))
+    ptr = _dense(w, "weight", dtype, index, (h,))
+    if ptr & 15:
+        raise ValueError("weight: must start on a multiple of 16 bytes")
+    return ptr, _DTYPES[dtype]
+
+
+def _logits(t, name: str, index: int) -> torch.dtype:
+    """Checks a matrix of logits; its type."""
+    if not isinstance(t, torch.Tensor) or t.dtype not in _DTYPES or t.dim() != 2:
+        _check(t, name, (_F32, _BF16), index, (None, None))
+    return t.dtype
 
 
 # ------------------------------------------------------------------ the norm
@@ -184,39 +261,36 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, *, residual: torch.Tensor | 
     Fp8Rows (packed, unless `out` gives other ones).  residual_out may be
     residual itself; without a residual no stream is returned.  save_rstd
     keeps what rms_norm_backward needs."""
-    dev = _device_of(x, "x")
-    _check(x, "x", _BF16, dev, (None, None))
-    T, H = x.shape
+    dev, index = _device_of(x, "x")
+    T, H = _matrix(x, "x", _BF16, index)
     _check_hidden(H)
     if not eps >= 0:
         raise ValueError(f"eps: {eps}, expected at least 0")
-    px, sx = _rows(x, "x", _BF16, dev, (T, H), 16)
+    shape = (T, H)
+    px, sx = _rows(x, "x", _BF16, index, shape, 16)
     pr = sr = po = so = pv = sv = ps = ss = ph = sh = pd = 0
     if residual is not None:
-        pr, sr = _rows(residual, "residual", _BF16, dev, (T, H), 16)
+        pr, sr = _rows(residual, "residual", _BF16, index, shape, 16)
         if residual_out is None:
-            residual_out = torch.empty((T, H), dtype=_BF16, device=dev)
-        ph, sh = _rows(residual_out, "residual_out", _BF16, dev, (T, H), 16)
+            residual_out = torch.empty(shape, dtype=_BF16, device=dev)
+        ph, sh = _rows(residual_out, "residual_out", _BF16, index, shape, 16)
     elif residual_out is not None:
         raise ValueError("residual_out: there is no residual")
-    pw = _dense(weight, "weight", (_BF16, _F32), dev, (H,))
-    if pw % 16:
-        raise ValueError("weight: must start on a multiple of 16 bytes")
+    pw, wtype = _weight(weight, index, H)
     if fp8:
         if out is None:
             out = Fp8Rows.empty(T, H, dev)
-        pv, sv, ps, ss = _fp8_rows(out, "out", dev, (T, H), 8)
+        pv, sv, ps, ss = _fp8_rows(out, "out", index, shape, 8)
     else:
         if out is None:
-            out = torch.empty((T, H), dtype=_BF16, device=dev)
-        po, so = _rows(out, "out", _BF16, dev, (T, H), 16)
+            out = torch.empty(shape, dtype=_BF16, device=dev)
+        po, so = _rows(out, "out", _BF16, index, shape, 16)
     rstd = None
     if save_rstd:
         rstd = torch.empty((T,), dtype=_F32, device=dev)
         pd = rstd.data_ptr()
     if T:
-        _call(dev, _ep.ep_rms_norm, T, H, px, sx, pr, sr, pw, _DTYPES[weight.dtype], eps, po, so, pv, sv, ps, ss,
-              ph, sh, pd)
+        _call(index, "ep_rms_norm", T, H, px, sx, pr, sr, pw, wtype, eps, po, so, pv, sv, ps, ss, ph, sh, pd)
     return Normed(out, residual_out, rstd)
 
 
@@ -228,36 +302,26 @@ def rms_norm_backward(dout: torch.Tensor, h: torch.Tensor, weight: torch.Tensor,
     its rstd.  dresidual: the gradient that reaches h directly.  dx, bf16
     [T, H], is the gradient of x and of residual alike and may be given as
     dout or dresidual; dweight is fp32 [H]."""
-    dev = _device_of(dout, "dout")
-    _check(dout, "dout", _BF16, dev, (None, None))
-    T, H = dout.shape
+    dev, index = _device_of(dout, "dout")
+    T, H = _matrix(dout, "dout", _BF16, index)
     _check_hidden(H)
-    pg, sg = _rows(dout, "dout", _BF16, dev, (T, H), 16)
-    ph, sh = _rows(h, "h", _BF16, dev, (T, H), 16)
-    pw = _dense(weight, "weight", (_BF16, _F32), dev, (H,))
-    if pw % 16:
-        raise ValueError("weight: must start on a multiple of 16 bytes")
-    pd = _dense(rstd, "rstd", _F32, dev, (T,))
+    shape = (T, H)
+    pg, sg = _rows(dout, "dout", _BF16, index, shape, 16)
+    ph, sh = _rows(h, "h", _BF16, index, shape, 16)
+    pw, wtype = _weight(weight, index, H)
+    pd = _dense(rstd, "rstd", _F32, index, (T,))
     pr = sr = 0
     if dresidual is not None:
-        pr, sr = _rows(dresidual, "dresidual", _BF16, dev, (T, H), 16)
+        pr, sr = _rows(dresidual, "dresidual", _BF16, index, shape, 16)
     if dx is None:
-        dx = torch.empty((T, H), dtype=_BF16, device=dev)
-    px, sx = _rows(dx, "dx", _BF16, dev, (T, H), 16)
+        dx = torch.empty(shape, dtype=_BF16, device=dev)
+    px, sx = _rows(dx, "dx", _BF16, index, shape, 16)
     dweight = torch.empty((H,), dtype=_F32, device=dev)
     size = _ep.ep_rms_norm_backward_workspace(T, H)
     work = torch.empty((size,), dtype=torch.uint8, device=dev)
-    _call(dev, _ep.ep_rms_norm_backward, T, H, pg, sg, ph, sh, pw, _DTYPES[weight.dtype], pd, pr, sr, px, sx,
-          dweight.data_ptr(), work.data_ptr(), size)
+    _call(index, "ep_rms_norm_backward", T, H, pg, sg, ph, sh, pw, wtype, pd, pr, sr, px, sx, dweight.data_ptr(),
+          work.data_ptr(), size)
     return dx, dweight
-
-
-def _fp8_rows(r, name: str, dev, shape, align: int) -> tuple[int, int, int, int]:
-    if not isinstance(r, Fp8Rows):
-        raise TypeError(f"{name}: expected Fp8Rows, got {type(r).__name__}")
-    pv, sv = _rows(r.values, name + ".values", _FP8, dev, shape, align)
-    ps, ss = _rows(r.scales, name + ".scales", _F32, dev, (r.values.shape[0], _blocks(r.values.shape[1])), 4)
-    return pv, sv, ps, ss
 
 
 # ---------------------------------------------------------------- the router
@@ -270,8 +334,8 @@ def route(logits: torch.Tensor, topk: int, *, renormalize: bool = True, token_ma
     False for padded tokens.  With balance_coef also the picks' counts per
     expert and the balance loss, and what route_backward needs.  With num_ranks
     also the weights with which EpLayer.combine adds the rows of pick_sum."""
-    dev = _device_of(logits, "logits")
-    _check(logits, "logits", (_F32, _BF16), dev, (None, None))
+    dev, index = _device_of(logits, "logits")
+    dtype = _logits(logits, "logits", index)
     T, E = logits.shape
     if not 1 <= E <= 4096:
         raise ValueError(f"logits: {E} experts, expected 1 to 4096")
@@ -279,13 +343,13 @@ def route(logits: torch.Tensor, topk: int, *, renormalize: bool = True, token_ma
         raise ValueError(f"topk: {topk}, expected 1 to {min(32, E)}")
     if num_ranks is not None and (num_ranks < 1 or E % num_ranks):
         raise ValueError(f"num_ranks: {num_ranks} does not divide {E} experts")
-    pl, sl = _rows(logits, "logits", (_F32, _BF16), dev, (T, E), logits.element_size())
-    pm = 0 if token_mask is None else _dense(token_mask, "token_mask", torch.bool, dev, (T,))
+    pl, sl = _rows(logits, "logits", dtype, index, (T, E), dtype.itemsize)
+    pm = 0 if token_mask is None else _dense(token_mask, "token_mask", torch.bool, index, (T,))
     idx = torch.empty((T, topk), dtype=_I32, device=dev)
     weights = torch.empty((T, topk), dtype=_F32, device=dev)
     ranked = None if num_ranks is None else torch.empty((T, topk), dtype=_F32, device=dev)
     count = loss = slope = lse = None
-    train = ()
+    train = (0.0, 0, 0, 0, 0, 0, 0)
     if balance_coef is not None:
         count = torch.empty((E,), dtype=_I32, device=dev)
         loss = torch.empty((), dtype=_F32, device=dev)
@@ -295,10 +359,9 @@ def route(logits: torch.Tensor, topk: int, *, renormalize: bool = True, token_ma
         work = torch.empty((size,), dtype=torch.uint8, device=dev)
         train = (balance_coef, lse.data_ptr(), count.data_ptr(), loss.data_ptr(), slope.data_ptr(), work.data_ptr(),
                  size)
-    if T or train:
-        _call(dev, _ep.ep_route, T, E, topk, pl, _DTYPES[logits.dtype], sl, pm, 1 if renormalize else 0,
-              idx.data_ptr(), weights.data_ptr(), num_ranks or 0, ranked.data_ptr() if ranked is not None else 0,
-              *(train or (0.0, 0, 0, 0, 0, 0, 0)))
+    if T or count is not None:
+        _call(index, "ep_route", T, E, topk, pl, _DTYPES[dtype], sl, pm, 1 if renormalize else 0, idx.data_ptr(),
+              weights.data_ptr(), num_ranks or 0, 0 if ranked is None else ranked.data_ptr(), *train)
     return Routing(idx, weights, ranked, count, loss, lse, slope, bool(renormalize))
 
 
@@ -307,27 +370,27 @@ def route_backward(logits: torch.Tensor, routing: Routing, dweights: torch.Tenso
     """ep_route_backward: the logits' gradient from those of the picks' weights
     (fp32 [T, K]) and of the balance loss (an fp32 scalar on the device; None:
     the loss was not used).  dlogits may be given as the logits."""
-    dev = _device_of(logits, "logits")
+    dev, index = _device_of(logits, "logits")
     if not isinstance(routing, Routing):
         raise TypeError(f"routing: expected a Routing, got {type(routing).__name__}")
     if routing.lse is None:
         raise ValueError("routing: made without balance_coef, it does not hold what the backward pass needs")
-    _check(logits, "logits", (_F32, _BF16), dev, (None, None))
+    dtype = _logits(logits, "logits", index)
     T, E = logits.shape
-    pl, sl = _rows(logits, "logits", (_F32, _BF16), dev, (T, E), logits.element_size())
+    pl, sl = _rows(logits, "logits", dtype, index, (T, E), dtype.itemsize)
     K = routing.topk_idx.shape[1]
     if dlogits is None:
-        dlogits = torch.empty((T, E), dtype=logits.dtype, device=dev)
-    pd, sd = _rows(dlogits, "dlogits", logits.dtype, dev, (T, E), logits.element_size())
-    args = (_dense(routing.topk_idx, "routing.topk_idx", _I32, dev, (T, K)),
-            _dense(routing.topk_weights, "routing.topk_weights", _F32, dev, (T, K)),
-            _dense(routing.lse, "routing.lse", _F32, dev, (T,)),
-            _dense(routing.slope, "routing.slope", _F32, dev, (E,)),
-            _dense(dweights, "dweights", _F32, dev, (T, K)),
-            0 if dloss is None else _dense(dloss, "dloss", _F32, dev, ()))
+        dlogits = torch.empty((T, E), dtype=dtype, device=dev)
+    pd, sd = _rows(dlogits, "dlogits", dtype, index, (T, E), dtype.itemsize)
+    args = (_dense(routing.topk_idx, "routing.topk_idx", _I32, index, (T, K)),
+            _dense(routing.topk_weights, "routing.topk_weights", _F32, index, (T, K)),
+            _dense(routing.lse, "routing.lse", _F32, index, (T,)),
+            _dense(routing.slope, "routing.slope", _F32, index, (E,)),
+            _dense(dweights, "dweights", _F32, index, (T, K)),
+            0 if dloss is None else _dense(dloss, "dloss", _F32, index, ()))
     if T:
-        _call(dev, _ep.ep_route_backward, T, E, K, pl, _DTYPES[logits.dtype], sl, 1 if routing.renormalize else 0,
-              *args, pd, sd)
+        _call(index, "ep_route_backward", T, E, K, pl, _DTYPES[dtype], sl, 1 if routing.renormalize else 0, *args, pd,
+              sd)
     return dlogits
 
 
@@ -347,44 +410,51 @@ def expert_product(a: Fp8Rows, w: torch.Tensor, w_scales: torch.Tensor, expert_o
     device, set to EP_ERR_INVALID_ARG where a place or row is out of range."""
     if not isinstance(a, Fp8Rows):
         raise TypeError(f"a: expected Fp8Rows, got {type(a).__name__}")
-    dev = _device_of(a.values, "a.values")
-    pa, sa, ps, ss = _fp8_rows(a, "a", dev, (None, None), 16)
-    A, K = a.values.shape
+    if a._buffer is not None:
+        dev, index = _device_of(a._buffer, "a")
+        A, K = a._buffer.shape[0], a._width
+    else:
+        dev, index = _device_of(a.values, "a.values")
+        A, K = _matrix(a.values, "a.values", _FP8, index)
+    pa, sa, ps, ss = _fp8_rows(a, "a", index, (A, K), 16)
     if not isinstance(w, torch.Tensor):
         raise TypeError(f"w: expected a torch.Tensor, got {type(w).__name__}")
-    gated = w.dim() == 4
-    if not gated and w.dim() != 3:
-        raise ValueError(f"w: shape {tuple(w.shape)}, expected [E, N, K] or [E, 2, N, K]")
-    E, N = w.shape[0], w.shape[-2]
+    shape = w.shape
+    gated = len(shape) == 4
+    if not gated and len(shape) != 3:
+        raise ValueError(f"w: shape {tuple(shape)}, expected [E, N, K] or [E, 2, N, K]")
+    E, N = shape[0], shape[-2]
     if K < 16 or K % 16 or K > 65536:
         raise ValueError(f"a: {K} columns, expected a multiple of 16 up to 65536")
     if N < 8 or N % 8 or N > 65536:
         raise ValueError(f"w: {N} rows, expected a multiple of 8 up to 65536")
     if not 1 <= E <= 4096:
         raise ValueError(f"w: {E} experts, expected 1 to 4096")
-    pair = (2,) if gated else ()
-    pw = _dense(w, "w", _FP8, dev, (E, *pair, N, K))
-    if pw % 16:
+    nb, kb = (N + BLOCK - 1) // BLOCK, (K + BLOCK - 1) // BLOCK
+    pw = _dense(w, "w", _FP8, index, (E, 2, N, K) if gated else (E, N, K))
+    if pw & 15:
         raise ValueError("w: must start on a multiple of 16 bytes")
-    pws = _dense(w_scales, "w_scales", _F32, dev, (E, *pair, _blocks(N), _blocks(K)))
-    off = _dense(expert_off, "expert_off", _I32, dev, (E,))
-    count = _dense(expert_count, "expert_count", _I32, dev, (E,))
+    pws = _dense(w_scales, "w_scales", _F32, index, (E, 2, nb, kb) if gated else (E, nb, kb))
+    off = _dense(expert_off, "expert_off", _I32, index, (E,))
+    count = _dense(expert_count, "expert_count", _I32, index, (E,))
     places, pr = A, 0
     if rows is not None:
-        pr = _dense(rows, "rows", _I32, dev, (None,))
+        if not isinstance(rows, torch.Tensor) or rows.dim() != 1:
+            _check(rows, "rows", _I32, index, (None,))
         places = rows.shape[0]
-    st = 0 if status is None else _dense(status, "status", _I32, dev, (1,))
+        pr = _dense(rows, "rows", _I32, index, (places,))
+    st = 0 if status is None else _dense(status, "status", _I32, index, (1,))
     po = so = pv = sv = pos = sos = 0
     if gated:
         if out is None:
             out = Fp8Rows.empty(places, N, dev)
-        pv, sv, pos, sos = _fp8_rows(out, "out", dev, (places, N), 8)
+        pv, sv, pos, sos = _fp8_rows(out, "out", index, (places, N), 8)
     else:
         if out is None:
             out = torch.empty((places, N), dtype=_BF16, device=dev)
-        po, so = _rows(out, "out", _BF16, dev, (places, N), 16)
+        po, so = _rows(out, "out", _BF16, index, (places, N), 16)
     if places:
-        _call(dev, _ep.ep_expert_product, places, A, E, K, N, 1 if gated else 0, pa, sa, ps, ss, pw, pws, off, count,
+        _call(index, "ep_expert_product", places, A, E, K, N, 1 if gated else 0, pa, sa, ps, ss, pw, pws, off, count,
               pr, po, so, pv, sv, pos, sos, st)
     return out
 
@@ -397,28 +467,30 @@ def pick_sum(y: torch.Tensor, recv_topk_idx: torch.Tensor, recv_topk_weights: to
     EpLayer.combine, taken with route's rank_weights.  The other arguments are
     fields of the Layout (recv_base, expert_off) and the ExpertLayout.
     status as in expert_product, for picks whose place is not found."""
-    dev = _device_of(y, "y")
-    _check(y, "y", _BF16, dev, (None, None))
-    M, H = y.shape
+    dev, index = _device_of(y, "y")
+    M, H = _matrix(y, "y", _BF16, index)
     if H < 8 or H % 8:
         raise ValueError(f"y: {H} columns, expected a multiple of 8")
-    py, sy = _rows(y, "y", _BF16, dev, (M, H), 16)
-    pi = _dense(recv_topk_idx, "recv_topk_idx", _I32, dev, (None, None))
-    N, K = recv_topk_idx.shape
-    pw = _dense(recv_topk_weights, "recv_topk_weights", _F32, dev, (N, K))
-    pb = _dense(recv_base, "recv_base", _I32, dev, (None,))
-    po = _dense(expert_off, "expert_off", _I32, dev, (None,))
+    py, sy = _rows(y, "y", _BF16, index, (M, H), 16)
+    N, K = _matrix(recv_topk_idx, "recv_topk_idx", _I32, index)
+    pi = _dense(recv_topk_idx, "recv_topk_idx", _I32, index, (N, K))
+    pw = _dense(recv_topk_weights, "recv_topk_weights", _F32, index, (N, K))
+    for t, name in ((recv_base, "recv_base"), (expert_off, "expert_off")):
+        if not isinstance(t, torch.Tensor) or t.dim() != 1:
+            _check(t, name, _I32, index, (None,))
     R, E = recv_base.shape[0], expert_off.shape[0]
+    pb = _dense(recv_base, "recv_base", _I32, index, (R,))
+    po = _dense(expert_off, "expert_off", _I32, index, (E,))
     if not 1 <= K <= 32:
         raise ValueError(f"recv_topk_idx: {K} picks, expected 1 to 32")
     if not 1 <= R <= 64 or E < R or E % R or E > 4096:
         raise ValueError(f"recv_base, expert_off: {R} ranks do not divide {E} experts")
-    pc = _dense(expert_count, "expert_count", _I32, dev, (E,))
-    pe = _dense(expert_rows, "expert_rows", _I32, dev, (M,))
-    st = 0 if status is None else _dense(status, "status", _I32, dev, (1,))
+    pc = _dense(expert_count, "expert_count", _I32, index, (E,))
+    pe = _dense(expert_rows, "expert_rows", _I32, index, (M,))
+    st = 0 if status is None else _dense(status, "status", _I32, index, (1,))
     if out is None:
         out = torch.empty((N, H), dtype=_BF16, device=dev)
-    pz, sz = _rows(out, "out", _BF16, dev, (N, H), 16)
+    pz, sz = _rows(out, "out", _BF16, index, (N, H), 16)
     if N:
-        _call(dev, _ep.ep_pick_sum, N, M, H, K, R, E, py, sy, pi, pw, pb, po, pc, pe, pz, sz, st)
+        _call(index, "ep_pick_sum", N, M, H, K, R, E, py, sy, pi, pw, pb, po, pc, pe, pz, sz, st)
     return out
