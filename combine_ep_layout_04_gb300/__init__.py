@@ -21,12 +21,12 @@ __all__ = [*_LAYER, "EpError", *_OPS]
 
 def __getattr__(name):
     if name in _LAYER:
-        from . import layer
-        return getattr(layer, name)
-    if name in _OPS:
-        from . import ops
-        return getattr(ops, name)
-    if name == "EpError":
-        from . import _ep
-        return _ep.EpError
-    raise AttributeError(name)
+        from . import layer as home
+    elif name in _OPS:
+        from . import ops as home
+    elif name == "EpError":
+        from . import _ep as home
+    else:
+        raise AttributeError(name)
+    value = globals()[name] = getattr(home, name)      # found here from now on
+    return value

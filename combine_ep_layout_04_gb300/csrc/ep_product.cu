@@ -240,6 +240,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(kGather),
     __shared__ int s_stop, s_scan[kThreads / 32];
     __shared__ float s_most[2][2][kRows];      // by turn, half, row
     __shared__ float s_x[kSlots][kRows], s_w[kSlots][2];      // scales of the rows, of the matrix blocks
+    __shared__ int s_tile[kSlots][3];          // first place, places and column tile, in the slot of a tile's first step
     uint8_t *stages = smem_raw + (-smem_u32(smem_raw) & 1023u);
     int *start = reinterpret_cast<int *>(stages + kStages * kStageBytes);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -407,6 +408,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(kGather),
 #pragma unroll
                         for (int j = 0; j < 4; ++j) s_x[slot][j * 32 + lane] = xs[j][i];
                         if (lane < 8 && (lane & 3) == i) s_w[slot][lane >> 2] = ws;
+                        if (k0 + i == 0 && lane == 0) s_tile[slot][0] = t.first, s_tile[slot][1] = t.here, s_tile[slot][2] = t.n;
                         __syncwarp();
                         // the sums learn of it by way of the step's products (a barrier of their own for
                         // it made a step of 0.51 us take 0.56)
@@ -480,17 +482,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(kGather),
             __syncwarp();
             if (lane == 0) arrive_cluster(first_cta(&bar.tempty[buf]));
         };
-        for (int id = cluster;; id += clusters) {
-            const Tile cur = tile_of(p, start, rank, id);
-            if (!cur.any) break;
-            const bool active = quad * 32 < cur.here && (kGated || cur.n * 2 + half < p.nb);
+        const int total = start[p.experts];
+        for (int id = cluster; id < total; id += clusters) {
+            int first = 0, here = 0, tile_n = 0;
+            bool active = false;
             unsigned long long acc[64];
 #pragma unroll
             for (int i = 0; i < 64; ++i) acc[i] = 0ull;
 #pragma unroll 1
             for (int kb = 0; kb < p.kb; ++kb, ++step) {
                 const int buf = half + 2 * (step & 1);       // this warp's accumulators: half, and half + 2
-                                if (!wait_for(&bar.tfull[buf], (step >> 1) & 1, &s_stop)) goto done;
+                if (!wait_for(&bar.tfull[buf], (step >> 1) & 1, &s_stop)) goto done;
+                if (kb == 0) {
+                    // what the tile is comes with its first scales: to look it up here left the products
+                    // waiting for it between tiles
+                    first = s_tile[step % kSlots][0], here = s_tile[step % kSlots][1], tile_n = s_tile[step % kSlots][2];
+                    active = quad * 32 < here && (kGated || tile_n * 2 + half < p.nb);
+                }
                 fence_after();
                 if (active) {
                     // 16 columns are read while the last 16 are added
@@ -512,15 +520,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(kGather),
                     accumulator_read(buf);
                 }
             }
-            const bool mine = row < cur.here;
-            const int64_t place = cur.first + row;
+            const bool mine = row < here;
+            const int64_t place = first + row;
             if (kGated) {
                 float y[64], most = kFloor;
 #pragma unroll
                 for (int i = 0; i < 64; ++i) {
                     const float g = i & 1 ? high_of(acc[i >> 1]) : low_of(acc[i >> 1]);
                     const float u = i & 1 ? high_of(acc[32 + (i >> 1)]) : low_of(acc[32 + (i >> 1)]);
-                    const int col = cur.n * kBlock + half * 64 + i;
+                    const int col = tile_n * kBlock + half * 64 + i;
                     y[i] = col < p.n ? __fdividef(g, 1.0f + __expf(-g)) * u : 0.0f;
                     most = max_nan(most, fabsf(y[i]));
                 }
@@ -533,9 +541,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(kGather),
                 turn ^= 1;
                 if (mine) {
                     const float inv = kFp8Max / most;
-                    if (half == 0) p.out_scales[place * p.out_scale_stride + cur.n] = most * (1.0f / kFp8Max);
-                    uint8_t *to = p.out_values + place * p.out_value_stride + cur.n * kBlock + half * 64;
-                    const int left = p.n - (cur.n * kBlock + half * 64);
+                    if (half == 0) p.out_scales[place * p.out_scale_stride + tile_n] = most * (1.0f / kFp8Max);
+                    uint8_t *to = p.out_values + place * p.out_value_stride + tile_n * kBlock + half * 64;
+                    const int left = p.n - (tile_n * kBlock + half * 64);
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
                         uint32_t v[8];
@@ -555,7 +563,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(kGather),
                     }
                 }
             } else if (mine && active) {
-                const int block = cur.n * 2 + half;
+                const int block = tile_n * 2 + half;
                 __nv_bfloat16 *to = p.out + place * p.out_stride + block * kBlock;
                 const int left = p.n - block * kBlock;
 #pragma unroll
