@@ -5,11 +5,13 @@
 // A warp holds a token's logits in registers, VPT to a lane, in vectors of V
 // neighbouring experts (V = 1 where a row's address or E does not allow more).
 // The K largest are found without sorting:
-//  - each lane's largest logit is known, and the K-th largest of these 32 (K
-//    warp-wide maxima) is a bound that at least K logits reach;
-//  - the few logits that reach it -- about K + 2 of 256 -- are written to
-//    shared memory as 64-bit words, the logit's bits in the floats' order and
-//    then the expert, so that ties go to the lower one;
+//  - the largest logit of each pair of lanes is known (of each lane for K > 16),
+//    and the K-th largest of these, from a bitonic sort across the lanes, is a
+//    bound that at least K logits reach (K warp-wide maxima in its place cost
+//    a third of the kernel);
+//  - the few logits that reach it -- about K + 3 of 256 -- are listed in shared
+//    memory as 64-bit words, the logit's bits in the floats' order and then the
+//    expert, so that ties go to the lower one;
 //  - each of them counts the words above its own: that is its place.
 // About 250 instructions a token and warp, where K rounds of a maximum over
 // all logits took 1800 (131072 tokens of 256 logits: 207 us, all issue).
@@ -48,7 +50,8 @@ __device__ __forceinline__ float key_value(uint32_t k) {
     return __uint_as_float((k & 0x80000000u) ? k & 0x7fffffffu : ~k);
 }
 
-constexpr int kWords = 64;         // words of a warp's list; a longer one (ties, wide K) takes the slow way
+constexpr int kWords = 64;         // words of a warp's list, two a lane; a longer one (ties, wide K) takes the slow way
+static_assert(kWords * sizeof(int) <= kMaxTopk * sizeof(unsigned long long), "the list's experts share the picks' room");
 
 __device__ __forceinline__ unsigned long long pick_word(float l, int e) {
     return (static_cast<unsigned long long>(order_key(l)) << 32) | static_cast<uint32_t>(~e);
@@ -96,46 +99,80 @@ __device__ __forceinline__ void load_row(const void *logits, int bf16, int64_t a
     }
 }
 
-// Lane k gets pick k's word, 0 where there is none; `top`: the largest key.
+// Sorts a value of each lane across the warp, largest first, by exchanges over
+// distances from kPair up (kPair = 2: lanes of a pair hold the same value).
+template <int kPair>
+__device__ __forceinline__ float sort_lanes(float v, int lane) {
+#pragma unroll
+    for (int k = 2 * kPair; k <= 32; k *= 2)
+#pragma unroll
+        for (int j = k / 2; j >= kPair; j /= 2) {
+            const float o = __shfl_xor_sync(0xffffffffu, v, j);
+            const bool larger = ((lane & j) == 0) == ((lane & k) == 0 || k == 32);
+            v = larger ? fmaxf(v, o) : fminf(v, o);
+        }
+    return v;
+}
+
+// Lane k gets pick k's word, 0 where there is none; top: the largest logit, or
+// -inf if none is above it.  row: the warp's room for the logits.
 template <int VPT, int V>
-__device__ __forceinline__ unsigned long long pick(const float (&l)[VPT], int K, int lane, unsigned long long *words,
-                                                   unsigned long long *picks, uint32_t &top) {
+__device__ __forceinline__ unsigned long long pick(const float (&l)[VPT], int E, int K, int lane, float *row,
+                                                   unsigned long long *words, unsigned long long *picks, float &top) {
     float most = l[0];
 #pragma unroll
     for (int j = 1; j < VPT; ++j) most = fmaxf(most, l[j]);      // NaN is passed over
-    uint32_t left = order_key(most), bound = 0;
-    top = __reduce_max_sync(0xffffffffu, left);
-    for (int k = 0; k < K; ++k) {
-        bound = k == 0 ? top : __reduce_max_sync(0xffffffffu, left);
-        if (bound == 0) break;
-        left = left == bound ? 0u : left;
+    most = most > -INFINITY ? most : -INFINITY;
+    float bound;
+    if (K <= 16) {
+        most = sort_lanes<2>(fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1)), lane);
+        bound = __shfl_sync(0xffffffffu, most, 2 * (K - 1));
+    } else {
+        most = sort_lanes<1>(most, lane);
+        bound = __shfl_sync(0xffffffffu, most, K - 1);
     }
-    // fewer than K different maxima: every logit above -inf is on the list
-    const float least = bound ? key_value(bound) : -3.402823466e38f;
-    // a lane's logits on the list, a bit each; lanes write one after another of theirs, most have none
+    top = __shfl_sync(0xffffffffu, most, 0);
+    // fewer than K of them: every logit above -inf is on the list
+    const float least = bound > -INFINITY ? bound : -3.402823466e38f;
+    // the logits where any lane can read them, and the experts on the list: a
+    // lane's have a bit each, and lanes write one after another of theirs (most
+    // have none)
+#pragma unroll
+    for (int j = 0; j < VPT; j += V) {
+        const int e = expert_of<V>(j, lane);
+        if (e < E) {
+            if constexpr (V == 4) *reinterpret_cast<float4 *>(row + e) = make_float4(l[j], l[j + 1], l[j + 2], l[j + 3]);
+            else if constexpr (V == 2) *reinterpret_cast<float2 *>(row + e) = make_float2(l[j], l[j + 1]);
+            else row[e] = l[j];
+        }
+    }
     int n = 0;
+    int *experts = reinterpret_cast<int *>(picks);
 #pragma unroll
     for (int j0 = 0; j0 < VPT; j0 += 32) {
         uint32_t on = 0;
 #pragma unroll
         for (int j = j0; j < VPT && j < j0 + 32; ++j) on |= l[j] >= least ? 1u << (j - j0) : 0u;
         for (uint32_t lanes = __ballot_sync(0xffffffffu, on != 0); lanes; lanes = __ballot_sync(0xffffffffu, on != 0)) {
-            const int j = __ffs(on) - 1, at = n + __popc(lanes & ((1u << lane) - 1u));
-            float v = l[j0];
-#pragma unroll
-            for (int i = j0 + 1; i < VPT && i < j0 + 32; ++i) v = i - j0 == j ? l[i] : v;
-            if (on && at < kWords) words[at] = pick_word(v, expert_of<V>(j0 + j, lane));
+            const int j = j0 + __ffs(on) - 1, at = n + __popc(lanes & ((1u << lane) - 1u));
+            if (on && at < kWords) experts[at] = expert_of<V>(j, lane);
             on &= on - 1;
             n += __popc(lanes);
         }
     }
-    if (lane < 4 && n <= kWords) words[n + lane] = 0;
+    __syncwarp();
+    const int listed = n <= kWords ? n : 0;
+    unsigned long long a = 0, b = 0;
+    if (lane < listed) a = pick_word(row[experts[lane]], experts[lane]);
+    if (lane + 32 < listed) b = pick_word(row[experts[lane + 32]], experts[lane + 32]);
+    __syncwarp();
+    words[lane] = a;                     // the list ends in zeros
+    words[lane + 32] = b;
     __syncwarp();
     unsigned long long mine = 0;
     if (n <= kWords) {
-        const unsigned long long a = lane < n ? words[lane] : 0, b = lane + 32 < n ? words[lane + 32] : 0;
         int above_a = 0, above_b = 0;
-        for (int q = 0; q < n; q += 4) {         // the list ends in four zeros
+        for (int q = 0; q < n; q += 4) {
             const ulonglong2 u = *reinterpret_cast<const ulonglong2 *>(words + q);
             const ulonglong2 v = *reinterpret_cast<const ulonglong2 *>(words + q + 2);
             const unsigned long long w[4] = {u.x, u.y, v.x, v.y};
@@ -176,11 +213,13 @@ __device__ __forceinline__ unsigned long long pick(const float (&l)[VPT], int K,
 
 template <int VPT, int V, bool kTrain>
 __global__ void __launch_bounds__(32 * kWarps, VPT <= 8 ? 4 : 1) route_kernel(RouteParams p) {
-    extern __shared__ float smem[];      // kTrain: p sums [kWarps][experts], then counts [experts]
-    __shared__ __align__(16) unsigned long long s_words[kWarps][kWords + 4], s_picks[kWarps][kMaxTopk];
+    // a row of logits, in the end of p sums, for each warp [kWarps][experts up to a multiple of 4]; kTrain: then
+    // counts [experts]
+    extern __shared__ __align__(16) float smem[];
+    __shared__ __align__(16) unsigned long long s_words[kWarps][kWords], s_picks[kWarps][kMaxTopk];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int E = p.experts, K = p.topk;
-    int32_t *count = reinterpret_cast<int32_t *>(smem + (kTrain ? kWarps * E : 0));
+    const int E = p.experts, K = p.topk, E4 = (E + 3) & ~3;
+    int32_t *count = reinterpret_cast<int32_t *>(smem + kWarps * E4);
     float psum[kTrain ? VPT : 1];
     int live_tokens = 0;
     if (kTrain) {
@@ -216,10 +255,10 @@ __global__ void __launch_bounds__(32 * kWarps, VPT <= 8 ? 4 : 1) route_kernel(Ro
             load_row<VPT, V>(p.logits, p.bf16, t * p.logits_stride, live ? E : 0, lane, l);
         }
         live_tokens += live;
-        uint32_t top;
-        const unsigned long long word = pick<VPT, V>(l, K, lane, s_words[warp], s_picks[warp], top);
+        float top;
+        const unsigned long long word = pick<VPT, V>(l, E, K, lane, smem + warp * E4, s_words[warp], s_picks[warp], top);
         const int my_e = word ? static_cast<int>(~static_cast<uint32_t>(word)) : -1;
-        const float most = top ? key_value(top) : 0.0f;
+        const float most = top > -INFINITY ? top : 0.0f;
         float sum = 0.0f;
         if (kTrain || !p.renormalize) {
 #pragma unroll
@@ -243,7 +282,7 @@ __global__ void __launch_bounds__(32 * kWarps, VPT <= 8 ? 4 : 1) route_kernel(Ro
         }
         if (kTrain) {
             if (my_e >= 0) atomicAdd(&count[my_e], 1);
-            if (lane == 0) p.lse[t] = live ? (top ? most + logf(sum) : sum != sum ? sum : -INFINITY) : INFINITY;
+            if (lane == 0) p.lse[t] = live ? (top > -INFINITY ? most + logf(sum) : sum != sum ? sum : -INFINITY) : INFINITY;
             const float inv = sum != 0.0f ? 1.0f / sum : 0.0f;
 #pragma unroll
             for (int j = 0; j < VPT; ++j) psum[j] = fmaf(l[j], inv, psum[j]);
@@ -252,13 +291,13 @@ __global__ void __launch_bounds__(32 * kWarps, VPT <= 8 ? 4 : 1) route_kernel(Ro
     if (kTrain) {
 #pragma unroll
         for (int j = 0; j < VPT; ++j)
-            if (expert_of<V>(j, lane) < E) smem[warp * E + expert_of<V>(j, lane)] = psum[j];
+            if (expert_of<V>(j, lane) < E) smem[warp * E4 + expert_of<V>(j, lane)] = psum[j];
         __shared__ int live_of[kWarps];
         if (lane == 0) live_of[warp] = live_tokens;
         __syncthreads();
         for (int e = threadIdx.x; e < E; e += blockDim.x) {
             float s = 0.0f;
-            for (int w = 0; w < kWarps; ++w) s += smem[w * E + e];
+            for (int w = 0; w < kWarps; ++w) s += smem[w * E4 + e];
             p.part_p[static_cast<int64_t>(blockIdx.x) * E + e] = s;
             p.part_count[static_cast<int64_t>(blockIdx.x) * E + e] = count[e];
         }
@@ -532,7 +571,7 @@ ep_status ep_route(int64_t tokens, int32_t experts, int32_t topk, const void *lo
         if (sms < 1) return EP_ERR_CUDA;
         const int64_t most = (tokens + kWarps - 1) / kWarps;
         const int grid = train ? blocks : static_cast<int>(most < 4 * sms ? most : 4 * sms);
-        const size_t smem = train ? sizeof(float) * experts * (kWarps + 1) : 0;
+        const size_t smem = sizeof(float) * ((experts + 3) / 4 * 4 * kWarps + (train ? experts : 0));
         by_width(experts, [&](int v) { return by_vector(logits, logits_stride, experts, p.bf16, v); },
                  [&](auto vpt, auto v) {
                      constexpr int VPT = decltype(vpt)::value, V = decltype(v)::value;
@@ -540,7 +579,8 @@ ep_status ep_route(int64_t tokens, int32_t experts, int32_t topk, const void *lo
                          allow_smem(route_kernel<VPT, V, true>, smem);
                          route_kernel<VPT, V, true><<<grid, 32 * kWarps, smem, st>>>(p);
                      } else {
-                         route_kernel<VPT, V, false><<<grid, 32 * kWarps, 0, st>>>(p);
+                         allow_smem(route_kernel<VPT, V, false>, smem);
+                         route_kernel<VPT, V, false><<<grid, 32 * kWarps, smem, st>>>(p);
                      }
                  });
     }
