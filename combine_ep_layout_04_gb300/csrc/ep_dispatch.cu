@@ -1611,8 +1611,10 @@ ep_status plan_dispatch(ep_ctx *h) {
     h->nbig = big_tok / chunk_tokens;
     h->nsmall = (Tpr - big_tok + small_tokens - 1) / small_tokens;
     h->nchunks = (h->nbig + h->nsmall) * R;
-    if (cudaFuncSetAttribute(dispatch_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             static_cast<int>(h->disp_smem)) != cudaSuccess)
+    // The limit belongs to the kernel, not to the handle: it is set to what any
+    // handle may use, so that a later handle that needs less does not lower it.
+    if (cudaFuncSetAttribute(dispatch_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, max_smem - reserve) !=
+        cudaSuccess)
         return EP_ERR_CUDA;
     int per_sm = 0;
     if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, dispatch_kernel, kThreads, h->disp_smem) !=

@@ -256,13 +256,14 @@ ep_status plan_expert_layout(ep_ctx *h) {
     const int64_t T = static_cast<int64_t>(h->cfg.num_ranks) * h->cfg.tokens_per_rank;
     const int E = h->cfg.num_experts, tile = expert_tile(E);
     h->xtiles = static_cast<int>((T + tile - 1) / tile);
-    const size_t smem = expert_smem_bytes(E);
-    if (smem > 48 * 1024) {
+    if (expert_smem_bytes(E) > 48 * 1024) {
+        // the limit belongs to the kernel, not to the handle: it is set to the most any handle uses
+        const size_t most = expert_smem_bytes(tile == kXTileLarge ? kXLargeMaxE : 4096);
         const bool k8 = h->cfg.topk <= 8;
-        const cudaError_t e = tile == kXTileLarge ? (k8 ? set_smem_limit<8, kXTileLarge>(smem)
-                                                        : set_smem_limit<32, kXTileLarge>(smem))
-                                                  : (k8 ? set_smem_limit<8, kXTileSmall>(smem)
-                                                        : set_smem_limit<32, kXTileSmall>(smem));
+        const cudaError_t e = tile == kXTileLarge ? (k8 ? set_smem_limit<8, kXTileLarge>(most)
+                                                        : set_smem_limit<32, kXTileLarge>(most))
+                                                  : (k8 ? set_smem_limit<8, kXTileSmall>(most)
+                                                        : set_smem_limit<32, kXTileSmall>(most));
         if (e != cudaSuccess) return EP_ERR_CUDA;
     }
     return EP_OK;
