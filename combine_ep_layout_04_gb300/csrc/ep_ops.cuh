@@ -3,6 +3,8 @@
 // bf16 and 8-bit packing, NaN-keeping maxima and row reductions on the device.
 #pragma once
 
+#include <atomic>
+
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 
@@ -25,11 +27,12 @@ struct Caller {
 
 // SMs of a device (read once per device; 0 if the runtime does not say).
 inline int sm_count_of(int device) {
-    static int known[64] = {};
-    if (device >= 0 && device < 64 && known[device]) return known[device];
-    int n = 0;
+    constexpr int kDevs = 64;
+    static std::atomic<int> known[kDevs];
+    int n = device >= 0 && device < kDevs ? known[device].load(std::memory_order_relaxed) : 0;
+    if (n) return n;
     if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, device) != cudaSuccess) return 0;
-    if (device >= 0 && device < 64) known[device] = n;
+    if (device >= 0 && device < kDevs) known[device].store(n, std::memory_order_relaxed);
     return n;
 }
 

@@ -641,12 +641,14 @@ ep_status launch_product(const ProductParams &p, int device, cudaStream_t st) {
     if (!encode(&amap, p.a_rows ? p.values : p.w, 2, adims, astride, abox) || !encode(&wmap, p.w, 4, wdims, wstride, wbox))
         return EP_ERR_CUDA;
     const size_t smem = 1024 + kStages * kStageBytes + sizeof(int) * (p.experts + 1);
-    static bool ready[64] = {};
-    if (device >= 64 || !ready[device]) {
+    // once a device: the most shared memory that any call takes
+    constexpr int kDevs = 64;
+    static std::atomic<bool> ready[kDevs];
+    if (device < 0 || device >= kDevs || !ready[device].load(std::memory_order_acquire)) {
         if (cudaFuncSetAttribute(product_kernel<kGated, kGather>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  1024 + kStages * kStageBytes + 4 * 4097) != cudaSuccess)
             return EP_ERR_CUDA;
-        if (device < 64) ready[device] = true;
+        if (device >= 0 && device < kDevs) ready[device].store(true, std::memory_order_release);
     }
     const int64_t ntiles = (p.n + (kGated ? kBlock : kTileN) - 1) / (kGated ? kBlock : kTileN);
     // every expert may leave one tile short

@@ -486,11 +486,13 @@ bool logits_ok(const void *p, int dtype, int64_t stride, int experts) {
            aligned(p, dtype == EP_DTYPE_F32 ? 4 : 2);
 }
 
-// Dynamic shared memory of a kernel, asked for where it is more than is given without asking.
+// Lets a kernel have the shared memory of the widest call, where this one
+// takes more than is given without asking.
 template <typename K>
 void allow_smem(K kernel, size_t bytes) {
     if (bytes > 48 * 1024)
-        (void)cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+        (void)cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                   static_cast<int>(sizeof(float)) * kMaxExperts * (kWarps + 1));
 }
 
 // Whether rows of logits can be taken V at a time.

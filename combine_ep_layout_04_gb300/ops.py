@@ -3,16 +3,16 @@ of the C ABI in include/ep_ops.h, whose kernels do all the arithmetic.
 
 A layer step with 8-bit rows, in the order of use:
 
-    n = rms_norm(x, weight, residual=res, fp8=True)        # 8-bit rows, new residual stream
-    r = route(logits, K, num_ranks=R)                      # picks and weights
-    lay = layer.layout(r.topk_idx)                         # layer: EpLayer(hidden=Fp8Rows.packed_width(H))
-    recv = layer.dispatch(n.out.packed, lay)               # values and scales travel as one row
-    xl = layer.expert_layout(r.topk_idx, r.topk_weights, lay)
+    n = rms_norm(x, weight, residual=res, fp8=True, with_bf16=True)
+    r = route(n.bf16 @ gate, K, num_ranks=R)               # picks and weights
+    lay = send.layout(r.topk_idx)                          # send: EpLayer with hidden = Fp8Rows.packed_width(H)
+    recv = send.dispatch(n.out.packed, lay)                # values and scales travel as one row
+    xl = send.expert_layout(r.topk_idx, r.topk_weights, lay)
     h = expert_product(Fp8Rows.from_packed(recv, H), w13, s13, lay.expert_off, xl.expert_count, rows=xl.expert_rows)
     y = expert_product(h, w2, s2, lay.expert_off, xl.expert_count)
     z = pick_sum(y, xl.recv_topk_idx, xl.recv_topk_weights, lay.recv_base, lay.expert_off, xl.expert_count,
                  xl.expert_rows)
-    out = layer2.combine(z, r.rank_weights, r.topk_idx, lay)
+    out = back.combine(z, r.rank_weights, r.topk_idx, lay)         # back: EpLayer with hidden = H
 
 Every call enqueues on the current stream of its tensors' device and returns
 without waiting; nothing is kept between calls.  A tensor of the wrong type
@@ -111,10 +111,12 @@ def _scales_at(width: int) -> int:
 @dataclasses.dataclass
 class Normed:
     """rms_norm's outputs: out is a bf16 tensor or Fp8Rows; residual is the new
-    residual stream (None without one); rstd fp32 [tokens] where asked for."""
+    residual stream (None without one); rstd fp32 [tokens] and bf16, the output
+    in bf16 beside the 8-bit one, where asked for."""
     out: torch.Tensor | Fp8Rows
     residual: torch.Tensor | None
     rstd: torch.Tensor | None
+    bf16: torch.Tensor | None = None
 
 
 @dataclasses.dataclass
@@ -254,13 +256,14 @@ def _logits(t, name: str, index: int) -> torch.dtype:
 # ------------------------------------------------------------------ the norm
 
 def rms_norm(x: torch.Tensor, weight: torch.Tensor, *, residual: torch.Tensor | None = None, eps: float = 1e-6,
-             fp8: bool = False, save_rstd: bool = False, out: torch.Tensor | Fp8Rows | None = None,
-             residual_out: torch.Tensor | None = None) -> Normed:
+             fp8: bool = False, with_bf16: bool = False, save_rstd: bool = False,
+             out: torch.Tensor | Fp8Rows | None = None, residual_out: torch.Tensor | None = None) -> Normed:
     """ep_rms_norm: h = x + residual, out = h / sqrt(mean(h^2) + eps) * weight.
     x, residual: bf16 [T, H]; weight: bf16 or fp32 [H].  With fp8 the output is
-    Fp8Rows (packed, unless `out` gives other ones).  residual_out may be
-    residual itself; without a residual no stream is returned.  save_rstd
-    keeps what rms_norm_backward needs."""
+    Fp8Rows (packed, unless `out` gives other ones), with_bf16 adds the same in
+    bf16 (for the router's logits).  residual_out may be residual itself;
+    without a residual no stream is returned.  save_rstd keeps what
+    rms_norm_backward needs."""
     dev, index = _device_of(x, "x")
     T, H = _matrix(x, "x", _BF16, index)
     _check_hidden(H)
@@ -269,6 +272,7 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, *, residual: torch.Tensor | 
     shape = (T, H)
     px, sx = _rows(x, "x", _BF16, index, shape, 16)
     pr = sr = po = so = pv = sv = ps = ss = ph = sh = pd = 0
+    both = None
     if residual is not None:
         pr, sr = _rows(residual, "residual", _BF16, index, shape, 16)
         if residual_out is None:
@@ -281,7 +285,12 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, *, residual: torch.Tensor | 
         if out is None:
             out = Fp8Rows.empty(T, H, dev)
         pv, sv, ps, ss = _fp8_rows(out, "out", index, shape, 8)
+        if with_bf16:
+            both = torch.empty(shape, dtype=_BF16, device=dev)
+            po, so = both.data_ptr(), H
     else:
+        if with_bf16:
+            raise ValueError("with_bf16: the output is bf16 already")
         if out is None:
             out = torch.empty(shape, dtype=_BF16, device=dev)
         po, so = _rows(out, "out", _BF16, index, shape, 16)
@@ -291,7 +300,7 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, *, residual: torch.Tensor | 
         pd = rstd.data_ptr()
     if T:
         _call(index, "ep_rms_norm", T, H, px, sx, pr, sr, pw, wtype, eps, po, so, pv, sv, ps, ss, ph, sh, pd)
-    return Normed(out, residual_out, rstd)
+    return Normed(out, residual_out, rstd, both)
 
 
 def rms_norm_backward(dout: torch.Tensor, h: torch.Tensor, weight: torch.Tensor, rstd: torch.Tensor, *,

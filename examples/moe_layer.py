@@ -1,0 +1,138 @@
+"""One Mixture-of-Experts layer with 8-bit rows and experts, end to end on one
+GPU: residual norm, router, layout, dispatch, the experts' products, the sum of
+each receive row's picks, combine.  And one training step of what is trained in
+higher precision: the router (with its balance loss) and the norm.
+
+    python examples/moe_layer.py [--tokens-per-rank 128] [--ranks 32] [--hidden 7168] [--experts 256] [--topk 8]
+                                 [--intermediate 2048] [--steps 20]
+
+The rows that travel are hidden + 4 * ceil(hidden / 128) bytes: the 8-bit
+values and their scales in one packed row, which the dispatch moves as it moves
+any row.  Prints the time of the layer and of its parts."""
+from __future__ import annotations
+
+import argparse
+import os
+import sys
+
+import torch
+
+sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+
+import combine_ep_layout_04_gb300 as ep  # noqa: E402
+
+BLOCK = 128
+
+
+def quantize_matrices(w: torch.Tensor) -> tuple[torch.Tensor, torch.Tensor]:
+    """Matrices [..., rows, columns] as e4m3 values and fp32 scales for each
+    block of 128 x 128 (done once, when weights are loaded)."""
+    rows, cols = w.shape[-2:]
+    pad = torch.nn.functional.pad(w.float(), (0, -cols % BLOCK, 0, -rows % BLOCK))
+    tiles = pad.unflatten(-1, (-1, BLOCK)).unflatten(-3, (-1, BLOCK))
+    scales = tiles.abs().amax((-3, -1)).clamp_min(2.0 ** -100) / 448
+    q = (tiles / scales[..., :, None, :, None]).clamp(-448, 448).flatten(-4, -3).flatten(-2)
+    return q[..., :rows, :cols].contiguous().to(torch.float8_e4m3fn), scales.contiguous()
+
+
+class MoeLayer:
+    """Weights and EP handles of a layer; every GPU buffer of a call is torch's."""
+
+    def __init__(self, ranks: int, tokens_per_rank: int, hidden: int, experts: int, topk: int, intermediate: int,
+                 seed: int = 0):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+
+        def rnd(*shape):
+            return torch.randn(*shape, device="cuda", generator=g)
+
+        self.ranks, self.hidden, self.topk = ranks, hidden, topk
+        self.norm = (1 + 0.1 * rnd(hidden)).to(torch.bfloat16)
+        self.gate = (rnd(hidden, experts) * hidden ** -0.5).to(torch.bfloat16)
+        up = [quantize_matrices(rnd(2, intermediate, hidden) * hidden ** -0.5) for _ in range(experts)]
+        down = [quantize_matrices(rnd(hidden, intermediate) * intermediate ** -0.5) for _ in range(experts)]
+        self.w13, self.s13 = (torch.stack(t) for t in zip(*up))
+        self.w2, self.s2 = (torch.stack(t) for t in zip(*down))
+        # rows go out packed in 8 bits and come back in bf16
+        self.send = ep.EpLayer(ranks, tokens_per_rank, ep.Fp8Rows.packed_width(hidden), experts, topk)
+        self.back = ep.EpLayer(ranks, tokens_per_rank, hidden, experts, topk)
+
+    def experts(self, rows: ep.Fp8Rows, lay: ep.Layout, xl: ep.ExpertLayout) -> torch.Tensor:
+        """The experts on the receive rows: one bf16 row per receive row."""
+        h = ep.expert_product(rows, self.w13, self.s13, lay.expert_off, xl.expert_count, rows=xl.expert_rows)
+        y = ep.expert_product(h, self.w2, self.s2, lay.expert_off, xl.expert_count)
+        return ep.pick_sum(y, xl.recv_topk_idx, xl.recv_topk_weights, lay.recv_base, lay.expert_off, xl.expert_count,
+                           xl.expert_rows)
+
+    def __call__(self, x: torch.Tensor, residual: torch.Tensor) -> tuple[torch.Tensor, torch.Tensor]:
+        """x, residual: bf16 [tokens, hidden].  Returns the layer's output and the new residual stream."""
+        n = ep.rms_norm(x, self.norm, residual=residual, fp8=True, with_bf16=True)
+        r = ep.route(n.bf16 @ self.gate, self.topk, num_ranks=self.ranks)
+        lay = self.send.layout(r.topk_idx)
+        recv = self.send.dispatch(n.out.packed, lay)
+        xl = self.send.expert_layout(r.topk_idx, r.topk_weights, lay)
+        z = self.experts(ep.Fp8Rows.from_packed(recv, self.hidden), lay, xl)
+        return self.back.combine(z, r.rank_weights, r.topk_idx, lay), n.residual
+
+    def train_step(self, x: torch.Tensor, residual: torch.Tensor, dweights, dy: torch.Tensor, balance_coef: float):
+        """Forward and backward of the norm and the router: from dweights (the
+        gradient of the picks' weights, as a function of the routing) and dy
+        (that of the normed rows by other ways) to the gradients of x, of the
+        norm's weight and of the gate, and the balance loss."""
+        n = ep.rms_norm(x, self.norm, residual=residual, save_rstd=True)
+        logits = n.out @ self.gate
+        r = ep.route(logits, self.topk, balance_coef=balance_coef)
+        dlogits = ep.route_backward(logits, r, dweights(r), torch.ones((), device=x.device))
+        dgate = n.out.t() @ dlogits
+        dx, dnorm = ep.rms_norm_backward(dy + dlogits @ self.gate.t(), n.residual, self.norm, n.rstd)
+        return dx, dnorm, dgate, r.balance_loss
+
+    def close(self) -> None:
+        self.send.close()
+        self.back.close()
+
+
+def main() -> None:
+    ap = argparse.ArgumentParser(description=__doc__, formatter_class=argparse.RawDescriptionHelpFormatter)
+    for name, default in (("ranks", 32), ("tokens-per-rank", 128), ("hidden", 7168), ("experts", 256), ("topk", 8),
+                          ("intermediate", 2048), ("steps", 20)):
+        ap.add_argument("--" + name, type=int, default=default)
+    a = ap.parse_args()
+    layer = MoeLayer(a.ranks, a.tokens_per_rank, a.hidden, a.experts, a.topk, a.intermediate)
+    tokens = a.ranks * a.tokens_per_rank
+    x, res = (torch.randn(tokens, a.hidden, device="cuda").to(torch.bfloat16) for _ in range(2))
+
+    def timed(f):
+        for _ in range(3):
+            f()
+        t0, t1 = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+        t0.record()
+        for _ in range(a.steps):
+            f()
+        t1.record()
+        t1.synchronize()
+        return t0.elapsed_time(t1) / a.steps * 1e3
+
+    out, _ = layer(x, res)
+    print(f"{tokens} tokens, hidden {a.hidden}, top {a.topk} of {a.experts} experts on {a.ranks} ranks")
+    print(f"layer: {timed(lambda: layer(x, res)):.1f} us")
+    n = ep.rms_norm(x, layer.norm, residual=res, fp8=True, with_bf16=True)
+    logits = n.bf16 @ layer.gate
+    r = ep.route(logits, a.topk, num_ranks=a.ranks)
+    lay = layer.send.layout(r.topk_idx)
+    recv = layer.send.dispatch(n.out.packed, lay)
+    xl = layer.send.expert_layout(r.topk_idx, r.topk_weights, lay)
+    rows = ep.Fp8Rows.from_packed(recv, a.hidden)
+    z = layer.experts(rows, lay, xl)
+    for name, f in (("norm", lambda: ep.rms_norm(x, layer.norm, residual=res, fp8=True, with_bf16=True)),
+                    ("router", lambda: ep.route(logits, a.topk, num_ranks=a.ranks)),
+                    ("layout", lambda: layer.send.layout(r.topk_idx, sync=False)),
+                    ("dispatch", lambda: layer.send.dispatch(n.out.packed, lay, recv=recv)),
+                    ("expert layout", lambda: layer.send.expert_layout(r.topk_idx, r.topk_weights, lay, out=xl)),
+                    ("experts", lambda: layer.experts(rows, lay, xl)),
+                    ("combine", lambda: layer.back.combine(z, r.rank_weights, r.topk_idx, lay, out=out))):
+        print(f"  {name}: {timed(f):.1f} us")
+    layer.close()
+
+
+if __name__ == "__main__":
+    main()

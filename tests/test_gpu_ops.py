@@ -581,3 +581,29 @@ def test_in_a_graph(ep):
     torch.cuda.synchronize()
     for a, b in zip(held, step()):
         assert torch.equal(a, b)
+
+
+def test_norm_in_8_bits_and_bf16_at_once(ep):
+    g = gen(61)
+    x, res, w = rnd(g, 40, 520, dtype=BF), rnd(g, 40, 520, dtype=BF), rnd(g, 520)
+    both = ep.rms_norm(x, w, residual=res, fp8=True, with_bf16=True)
+    eight, plain = ep.rms_norm(x, w, residual=res, fp8=True), ep.rms_norm(x, w, residual=res)
+    assert torch.equal(both.bf16, plain.out)
+    assert torch.equal(both.out.values.float(), eight.out.values.float())
+    assert torch.equal(both.out.scales, eight.out.scales) and plain.bf16 is None
+    with pytest.raises(ValueError):
+        ep.rms_norm(x, w, with_bf16=True)
+
+
+def test_packed_rows_travel_as_one_piece(ep):
+    """A packed row's bytes are its values, then its scales, on the widths a dispatch takes."""
+    g = gen(62)
+    for width in (8, 136, 256, 1000, 7168):
+        a = ep.Fp8Rows.empty(5, width)
+        assert a.packed.shape == (5, ep.Fp8Rows.packed_width(width)) and a.packed.shape[1] % 8 == 0
+        a.packed.zero_()
+        a.values.copy_(rnd(g, 5, width))
+        a.scales.copy_(rnd(g, *a.scales.shape))
+        b = ep.Fp8Rows.from_packed(a.packed.clone(), width)
+        assert torch.equal(b.values.float(), a.values.float()) and torch.equal(b.scales, a.scales)
+        assert torch.equal(b.float(), a.float())
