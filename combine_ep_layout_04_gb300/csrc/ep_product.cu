@@ -140,9 +140,12 @@ __device__ __forceinline__ void load_2d(void *dst, const CUtensorMap *map, int x
         "l"(map), "r"(x), "r"(y), "r"(bar)
         : "memory");
 }
-// 16 bytes, or zeros without a source
-__device__ __forceinline__ void fetch16(uint32_t dst, const void *src, bool there) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+// 16 bytes of row r, `bytes` of them read and the rest zeros
+__device__ __forceinline__ void fetch16(uint32_t dst, const void *rows, int r, uint32_t stride, int bytes) {
+    asm volatile(
+        "{\n\t.reg .b64 a;\n\tmad.wide.u32 a, %2, %3, %1;\n\tcp.async.cg.shared.global [%0], [a], 16, %4;\n\t}" ::"r"(dst),
+        "l"(rows), "r"(r), "r"(stride), "r"(bytes)
+        : "memory");
 }
 __device__ __forceinline__ bool elected() {
     uint32_t ok;
@@ -185,11 +188,16 @@ __device__ __forceinline__ void read16(uint32_t at, uint32_t (&r)[16]) {
         : "memory");
 }
 __device__ __forceinline__ void read_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
-// sums of two neighbouring columns: acc += v * s
-__device__ __forceinline__ void add_pair(unsigned long long &acc, uint32_t v0, uint32_t v1, float s) {
-    asm volatile("{\n\t.reg .b64 v, s;\n\tmov.b64 v, {%1, %2};\n\tmov.b64 s, {%3, %3};\n\tfma.rn.f32x2 %0, v, s, %0;\n\t}"
-        : "+l"(acc)
-        : "r"(v0), "r"(v1), "r"(__float_as_uint(s)));
+// a factor for both of two neighbouring columns, and their sums: acc += v * s
+__device__ __forceinline__ unsigned long long twice(float s) {
+    unsigned long long d;
+    asm("mov.b64 %0, {%1, %1};" : "=l"(d) : "r"(__float_as_uint(s)));
+    return d;
+}
+__device__ __forceinline__ void add_pair(unsigned long long &acc, uint32_t v0, uint32_t v1, unsigned long long s) {
+    asm volatile("{\n\t.reg .b64 v;\n\tmov.b64 v, {%1, %2};\n\tfma.rn.f32x2 %0, v, %3, %0;\n\t}"
+                 : "+l"(acc)
+                 : "r"(v0), "r"(v1), "l"(s));
 }
 __device__ __forceinline__ float low_of(unsigned long long v) { return __uint_as_float(static_cast<uint32_t>(v)); }
 __device__ __forceinline__ float high_of(unsigned long long v) { return __uint_as_float(static_cast<uint32_t>(v >> 32)); }
@@ -424,30 +432,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(kGather),
         // ---- places' rows from anywhere: eight threads a row of 128 bytes, kGatherRows rows a thread.
         // A stage is handed over kGatherLag blocks later, when its copies are complete.
         constexpr int kStride = kGatherWarps * 4;        // rows that the warps fetch at once
-        const int i = tid - 32 * (4 + kSums), sub = i >> 3, seg = i & 7;
+        const uint32_t stride = static_cast<uint32_t>(p.value_stride);
         const uint8_t *base = p.a_rows > 0 ? p.values : p.w;
+        const int i = tid - 32 * (4 + kSums), sub = i >> 3, seg = i & 7;
         int stage = 0, lagging = 0, late = 0;       // stages not yet handed over, the first of them
         uint32_t phase = 0;
         for (int id = cluster;; id += clusters) {
             const Tile t = tile_of(p, start, rank, id);
             if (!t.any) break;
             int src[kGatherRows];
+            uint32_t there = 0;              // a bit for each row that is; another one's values are zeros
 #pragma unroll
             for (int j = 0; j < kGatherRows; ++j) {
-                src[j] = sub + kStride * j < t.here ? p.rows[t.first + sub + kStride * j] : -1;
-                if (src[j] >= p.a_rows) src[j] = -1;
+                const int m = sub + kStride * j;
+                src[j] = m < t.here ? p.rows[t.first + m] : -1;
+                if (src[j] < 0 || src[j] >= p.a_rows) src[j] = 0;
+                else there |= 1u << j;
             }
             const int steps = (t.here + kStride - 1) / kStride;
             for (int kb = 0; kb < p.kb; ++kb) {
                 if (!wait_for(&bar.empty[stage], phase ^ 1u, &s_stop)) goto done;
                 const uint32_t to = smem_u32(stages + stage * kStageBytes) + sub * 128 + ((seg ^ (sub & 7)) << 4);
                 const int col = kb * kBlock + seg * 16;
+                const uint32_t some = col < p.width ? there : 0u;
 #pragma unroll
                 for (int j = 0; j < kGatherRows; ++j)
-                    if (j < steps) {
-                        const bool there = src[j] >= 0 && col < p.width;
-                        fetch16(to + j * kStride * 128, there ? base + src[j] * p.value_stride + col : base, there);
-                    }
+                    if (j < steps)
+                        fetch16(to + j * kStride * 128, some ? base + col : base, src[j], stride, (some >> j & 1u) << 4);
                 asm volatile("cp.async.commit_group;" ::: "memory");
                 if (lagging == kGatherLag) {
                     asm volatile("cp.async.wait_group %0;" ::"n"(kGatherLag) : "memory");
@@ -506,7 +517,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(kGather),
                     uint32_t v[2][16];
                     read16(at, v[0]);
                     const float x = s_x[step % kSlots][row];
-                    const float s0 = x * s_w[step % kSlots][kGated ? 0 : half], s1 = kGated ? x * s_w[step % kSlots][1] : s0;
+                    const unsigned long long s0 = twice(x * s_w[step % kSlots][kGated ? 0 : half]);
+                    const unsigned long long s1 = kGated ? twice(x * s_w[step % kSlots][1]) : s0;
 #pragma unroll
                     for (int c = 0; c < 8; ++c) {
                         read_wait();
@@ -675,7 +687,8 @@ extern "C" ep_status ep_expert_product(int64_t places, int64_t a_rows, int32_t e
     if (!w || !w_scales || !expert_off || !expert_count || (a_rows > 0 && (!values || !scales)) ||
         (!rows && places > a_rows))
         return EP_ERR_INVALID_ARG;
-    if (!aligned(values, 16) || value_stride % 16 != 0 || value_stride < width || !aligned(scales, 4) ||
+    if (!aligned(values, 16) || value_stride % 16 != 0 || value_stride < width ||
+        value_stride >= (1ll << 31) || !aligned(scales, 4) ||
         scale_stride < kb || !aligned(w, 16) || !aligned(w_scales, 4))
         return EP_ERR_INVALID_ARG;
     if (gated ? !out_values || !out_scales || out_bf16 || !aligned(out_values, 8) || out_value_stride % 8 != 0 ||
