@@ -35,14 +35,14 @@ bool ptr_usable_on(int device, const void *p) {
 // pointer value: callers pass the same buffers call after call, so the
 // runtime is asked once per buffer.
 bool ptr_usable_cached(int device, const void *p) {
-    constexpr int kSlots = 64;
+    constexpr int kBits = 10;          // a step's buffers rarely share a slot of 1024
     struct Slot {
         uintptr_t ptr;
         int device;
     };
-    thread_local Slot cache[kSlots] = {};
+    thread_local Slot cache[1 << kBits] = {};
     const uintptr_t v = reinterpret_cast<uintptr_t>(p);
-    Slot &slot = cache[((v >> 8) ^ (v >> 20)) % kSlots];
+    Slot &slot = cache[(v * 0x9E3779B97F4A7C15ull) >> (64 - kBits)];
     if (slot.ptr == v && slot.device == device) return true;
     if (!ptr_usable_on(device, p)) return false;
     slot = Slot{v, device};
