@@ -202,6 +202,15 @@ __device__ __forceinline__ void add_pair(unsigned long long &acc, uint32_t v0, u
 __device__ __forceinline__ float low_of(unsigned long long v) { return __uint_as_float(static_cast<uint32_t>(v)); }
 __device__ __forceinline__ float high_of(unsigned long long v) { return __uint_as_float(static_cast<uint32_t>(v >> 32)); }
 
+// g / (1 + exp(-g)): two special-function operations and three more, within a
+// few units of the last place (an exp(-g) that overflows gives 0).
+__device__ __forceinline__ float silu(float g) {
+    float e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.4426950408889634f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
+    return g * r;
+}
+
 // 32 bytes to one row, in one store where rows start on 32-byte boundaries.
 __device__ __forceinline__ void store32(void *to, const uint32_t (&v)[8], bool wide) {
     if (wide) {
@@ -532,18 +541,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(kGather),
                     accumulator_read(buf);
                 }
             }
+            if (!active) continue;       // neither of the two warps of these rows is, gated
             const bool mine = row < here;
             const int64_t place = first + row;
             if (kGated) {
-                float y[64], most = kFloor;
+                // The products wait for this, two steps ahead at most: four maxima side by side, and no
+                // comparison of columns but in the last tile of a width that 128 does not divide.
+                float y[64], m[4] = {kFloor, kFloor, kFloor, kFloor};
+                const int left = p.n - (tile_n * kBlock + half * 64);
 #pragma unroll
                 for (int i = 0; i < 64; ++i) {
                     const float g = i & 1 ? high_of(acc[i >> 1]) : low_of(acc[i >> 1]);
                     const float u = i & 1 ? high_of(acc[32 + (i >> 1)]) : low_of(acc[32 + (i >> 1)]);
-                    const int col = tile_n * kBlock + half * 64 + i;
-                    y[i] = col < p.n ? __fdividef(g, 1.0f + __expf(-g)) * u : 0.0f;
-                    most = max_nan(most, fabsf(y[i]));
+                    y[i] = silu(g) * u;
                 }
+                if (left < 64) {
+#pragma unroll
+                    for (int i = 0; i < 64; ++i) y[i] = i < left ? y[i] : 0.0f;
+                }
+#pragma unroll
+                for (int i = 0; i < 64; ++i) m[i & 3] = max_nan(m[i & 3], fabsf(y[i]));
+                float most = max_nan(max_nan(m[0], m[1]), max_nan(m[2], m[3]));
                 // the other half's maximum; two turns, as a warp may be a tile ahead when the other one reads
                 s_most[turn][half][row] = most;
                 __syncwarp();
@@ -555,7 +573,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(kGather),
                     const float inv = kFp8Max / most;
                     if (half == 0) p.out_scales[place * p.out_scale_stride + tile_n] = most * (1.0f / kFp8Max);
                     uint8_t *to = p.out_values + place * p.out_value_stride + tile_n * kBlock + half * 64;
-                    const int left = p.n - (tile_n * kBlock + half * 64);
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
                         uint32_t v[8];
@@ -574,7 +591,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(kGather),
                         }
                     }
                 }
-            } else if (mine && active) {
+            } else if (mine) {
                 const int block = tile_n * 2 + half;
                 __nv_bfloat16 *to = p.out + place * p.out_stride + block * kBlock;
                 const int left = p.n - block * kBlock;

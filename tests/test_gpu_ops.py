@@ -320,6 +320,14 @@ def test_product(ep, counts, N, K, gated, gather):
         check_product(ep, rows8(g, ep, M, K), w, s, off, count)
 
 
+@pytest.mark.parametrize("counts", [[129], [300, 0, 400, 1], [513, 130], [256, 257]])
+@pytest.mark.parametrize("N,K", [(8, 16), (72, 272), (136, 144), (264, 400), (512, 1024)])
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("gather", [False, True])
+def test_product_many_places_to_an_expert(ep, counts, N, K, gated, gather):
+    test_product(ep, counts, N, K, gated, gather)
+
+
 @pytest.mark.parametrize("gated", [False, True])
 def test_product_long_rows_many_experts(ep, gated):
     g = gen(31)
