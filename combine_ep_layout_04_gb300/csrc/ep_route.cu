@@ -309,9 +309,12 @@ __global__ void __launch_bounds__(32 * kWarps, VPT <= 8 ? 4 : 1) route_kernel(Ro
     }
 }
 
-// Adds the blocks' sums in order and makes counts, slope and loss: 32 experts
-// to a block, 32 warps that take every 32nd of the routing blocks.  The last
-// block to finish adds the blocks' parts of the loss, in order too.
+// Adds the blocks' sums in order and makes counts, slope and loss: 8 experts to
+// a block, 128 of the routing blocks at a time -- four to a warp, added by
+// shuffles.  The last block to finish adds the blocks' parts of the loss, in
+// order too.
+constexpr int kBalanceExperts = 8;
+
 struct BalanceParams {
     const float *part_p;
     const int32_t *part_count, *part_live;
@@ -324,45 +327,58 @@ struct BalanceParams {
 };
 
 __global__ void __launch_bounds__(1024) balance_kernel(BalanceParams p) {
-    __shared__ float s_p[32][33];
-    __shared__ int s_n[32][33], s_live[32];
-    __shared__ bool s_last;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, e = blockIdx.x * 32 + lane;
+    __shared__ float s_p[kBalanceExperts][33];
+    __shared__ int s_n[kBalanceExperts][33], s_live[32];
+    __shared__ float s_loss[kBalanceExperts];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, e = blockIdx.x * kBalanceExperts + (lane & 7);
     int live = 0;
     for (int b = tid; b < p.parts; b += 1024) live += p.part_live[b];
     float s = 0.0f;
     int n = 0;
     if (e < p.experts) {
-#pragma unroll 8
-        for (int b = warp; b < p.parts; b += 32) {
+        for (int b = warp * 4 + (lane >> 3); b < p.parts; b += 128) {
             s += p.part_p[static_cast<int64_t>(b) * p.experts + e];
             n += p.part_count[static_cast<int64_t>(b) * p.experts + e];
         }
     }
-    s_p[warp][lane] = s;
-    s_n[warp][lane] = n;
+#pragma unroll
+    for (int o = 8; o <= 16; o *= 2) {
+        s += __shfl_xor_sync(0xffffffffu, s, o);
+        n += __shfl_xor_sync(0xffffffffu, n, o);
+    }
+    if (lane < kBalanceExperts) {
+        s_p[lane][warp] = s;
+        s_n[lane][warp] = n;
+    }
     live = __reduce_add_sync(0xffffffffu, live);
     if (lane == 0) s_live[warp] = live;
     __syncthreads();
-    if (warp == 0) {
+    if (warp < kBalanceExperts) {
         live = __reduce_add_sync(0xffffffffu, s_live[lane]);
         const float tv = live > 0 ? static_cast<float>(live) : 1.0f;
         const float scale = p.coef * static_cast<float>(p.experts) / (static_cast<float>(p.topk) * tv * tv);
-        s = 0.0f;
-        n = 0;
-        for (int w = 0; w < 32; ++w) s += s_p[w][lane], n += s_n[w][lane];
+        s = warp_sum(s_p[warp][lane]);
+        n = __reduce_add_sync(0xffffffffu, s_n[warp][lane]);
+        const int mine = blockIdx.x * kBalanceExperts + warp;
         const float g = scale * static_cast<float>(n);
-        if (e < p.experts) {
-            p.expert_count[e] = n;
-            p.slope[e] = g;
-        }
-        s = warp_sum(e < p.experts ? g * s : 0.0f);
         if (lane == 0) {
-            p.part_loss[blockIdx.x] = s;
-            s_last = atom_add_acq_rel(p.done, 1u) == gridDim.x - 1;
+            if (mine < p.experts) {
+                p.expert_count[mine] = n;
+                p.slope[mine] = g;
+            }
+            s_loss[warp] = mine < p.experts ? g * s : 0.0f;
         }
-        __syncwarp();
-        if (s_last) {
+    }
+    __syncthreads();
+    if (warp == 0) {
+        bool last = false;
+        if (lane == 0) {
+            s = 0.0f;
+            for (int i = 0; i < kBalanceExperts; ++i) s += s_loss[i];
+            p.part_loss[blockIdx.x] = s;
+            last = atom_add_acq_rel(p.done, 1u) == gridDim.x - 1;
+        }
+        if (__shfl_sync(0xffffffffu, last, 0)) {
             s = 0.0f;
             for (int b = lane; b < static_cast<int>(gridDim.x); b += 32)
                 s += *static_cast<volatile const float *>(p.part_loss + b);
@@ -475,7 +491,7 @@ int route_blocks(int64_t tokens) {
     return static_cast<int>(want < kTrainBlocks ? want : kTrainBlocks);
 }
 
-int balance_blocks(int experts) { return (experts + 31) / 32; }
+int balance_blocks(int experts) { return (experts + kBalanceExperts - 1) / kBalanceExperts; }
 
 bool sizes_ok(int64_t tokens, int experts, int topk) {
     return tokens >= 0 && tokens < (1ll << 31) && experts >= 1 && experts <= kMaxExperts && topk >= 1 &&
