@@ -229,24 +229,24 @@ __global__ void __launch_bounds__(32 * kWarps, VPT <= 8 ? 4 : 1) route_kernel(Ro
         for (int j = 0; j < VPT; ++j) psum[j] = 0.0f;
         __syncthreads();
     }
-    const int64_t stride = static_cast<int64_t>(gridDim.x) * kWarps;
-    int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
+    const uint32_t T = static_cast<uint32_t>(p.tokens), stride = gridDim.x * kWarps;
+    uint32_t t = blockIdx.x * kWarps + warp;
     // a token's logits are on their way while the last one's are worked on, where they fit twice
     constexpr bool kAhead = VPT <= 16;
     float ahead[kAhead ? VPT : 1];
     bool live_ahead = false;
-    if (kAhead && t < p.tokens) {
+    if (kAhead && t < T) {
         live_ahead = p.mask == nullptr || p.mask[t] != 0;
         if constexpr (kAhead) load_row<VPT, V>(p.logits, p.bf16, t * p.logits_stride, live_ahead ? E : 0, lane, ahead);
     }
-    for (; t < p.tokens; t += stride) {
+    for (; t < T; t += stride) {
         float l[VPT];
         bool live;
         if constexpr (kAhead) {
             live = live_ahead;
 #pragma unroll
             for (int j = 0; j < VPT; ++j) l[j] = ahead[j];
-            if (t + stride < p.tokens) {
+            if (t + stride < T) {
                 live_ahead = p.mask == nullptr || p.mask[t + stride] != 0;
                 load_row<VPT, V>(p.logits, p.bf16, (t + stride) * p.logits_stride, live_ahead ? E : 0, lane, ahead);
             }
@@ -271,14 +271,15 @@ __global__ void __launch_bounds__(32 * kWarps, VPT <= 8 ? 4 : 1) route_kernel(Ro
         float w = word ? __expf(key_value(static_cast<uint32_t>(word >> 32)) - most) : 0.0f;
         const float total = p.renormalize ? warp_sum(w) : sum;
         w = word ? __fdividef(w, total) : 0.0f;      // total is 1 .. experts, or NaN
+        const uint64_t at = static_cast<uint64_t>(t) * static_cast<uint32_t>(K) + lane;
         if (lane < K) {
-            p.topk_idx[t * K + lane] = my_e;
-            p.topk_weights[t * K + lane] = w;
+            p.topk_idx[at] = my_e;
+            p.topk_weights[at] = w;
         }
         if (p.rank_weights) {
             const int rank = my_e >= 0 ? my_e / p.per_rank : -1 - lane;
             const uint32_t same = __match_any_sync(0xffffffffu, rank);
-            if (lane < K) p.rank_weights[t * K + lane] = my_e >= 0 && __ffs(same) - 1 == lane ? 1.0f : 0.0f;
+            if (lane < K) p.rank_weights[at] = my_e >= 0 && __ffs(same) - 1 == lane ? 1.0f : 0.0f;
         }
         if (kTrain) {
             if (my_e >= 0) atomicAdd(&count[my_e], 1);
@@ -418,24 +419,25 @@ __global__ void __launch_bounds__(32 * kWarps, VPT <= 8 ? 4 : 1) route_grad_kern
         for (int j = 0; j < VPT; ++j)
             slope[j] = p.dloss && expert_of<V>(j, lane) < E ? dloss * p.slope[expert_of<V>(j, lane)] : 0.0f;
     }
-    const int64_t stride = static_cast<int64_t>(gridDim.x) * kWarps;
-    int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
+    const uint32_t T = static_cast<uint32_t>(p.tokens), stride = gridDim.x * kWarps;
+    uint32_t t = blockIdx.x * kWarps + warp;
     // A token's inputs are on their way while the last one's are worked on.
     // lse is +inf for a padded token and -inf where no logit was left: both
     // have p = 0, whatever the logits hold.
     float ahead[VPT], lse_ahead = 0.0f, w_ahead = 0.0f, add_ahead = 0.0f;
     int idx_ahead = -1;
-    auto fetch = [&](int64_t at) {
+    auto fetch = [&](uint32_t at) {
         lse_ahead = p.lse[at];
         load_row<VPT, V>(p.logits, p.bf16, at * p.logits_stride, E, lane, ahead);
+        const uint64_t pick = static_cast<uint64_t>(at) * static_cast<uint32_t>(K) + lane;
         if (lane < K) {
-            idx_ahead = p.topk_idx[at * K + lane];
-            w_ahead = p.topk_weights[at * K + lane];
-            add_ahead = p.dweights[at * K + lane];
+            idx_ahead = p.topk_idx[pick];
+            w_ahead = p.topk_weights[pick];
+            add_ahead = p.dweights[pick];
         }
     };
-    if (t < p.tokens) fetch(t);
-    for (; t < p.tokens; t += stride) {
+    if (t < T) fetch(t);
+    for (; t < T; t += stride) {
         const float lse = lse_ahead;
         const bool live = !isinf(lse);
         float l[VPT];
@@ -443,7 +445,7 @@ __global__ void __launch_bounds__(32 * kWarps, VPT <= 8 ? 4 : 1) route_grad_kern
         for (int j = 0; j < VPT; ++j) l[j] = ahead[j];
         const int idx = idx_ahead;
         float w = idx >= 0 ? w_ahead : 0.0f, add = idx >= 0 ? add_ahead : 0.0f;
-        if (t + stride < p.tokens) fetch(t + stride);
+        if (t + stride < T) fetch(t + stride);
         if (p.renormalize) add = w * (add - warp_sum(w * add));
         if (idx >= 0 && idx < E) picks[idx] = add;
         __syncwarp();
