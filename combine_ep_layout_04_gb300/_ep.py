@@ -294,35 +294,11 @@ def ep_sm_ids(stream: int, blocks: int, out_ptr: int) -> None:
 
 
 # ------------------------------------------------ operators (include/ep_ops.h)
-# Arguments in the header's order; pointers and streams are whole numbers, None is NULL.
-
-def ep_rms_norm(*args) -> None:
-    check(lib.ep_rms_norm(*args), "ep_rms_norm")
-
+# The calls themselves are made by ops.py on `lib`.
 
 def ep_rms_norm_backward_workspace(tokens: int, hidden: int) -> int:
     return lib.ep_rms_norm_backward_workspace(tokens, hidden)
 
 
-def ep_rms_norm_backward(*args) -> None:
-    check(lib.ep_rms_norm_backward(*args), "ep_rms_norm_backward")
-
-
 def ep_route_workspace(tokens: int, experts: int) -> int:
     return lib.ep_route_workspace(tokens, experts)
-
-
-def ep_route(*args) -> None:
-    check(lib.ep_route(*args), "ep_route")
-
-
-def ep_route_backward(*args) -> None:
-    check(lib.ep_route_backward(*args), "ep_route_backward")
-
-
-def ep_expert_product(*args) -> None:
-    check(lib.ep_expert_product(*args), "ep_expert_product")
-
-
-def ep_pick_sum(*args) -> None:
-    check(lib.ep_pick_sum(*args), "ep_pick_sum")

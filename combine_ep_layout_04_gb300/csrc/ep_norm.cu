@@ -6,8 +6,12 @@
 // and writes one (8 bytes a value).  A row stays in registers between the pass
 // that sums it and the pass that uses the sum, so nothing is read twice: a
 // team of warps holds a row, eight neighbouring values (16 bytes) to a lane in
-// each of VPT steps.  Rows up to 1024 columns take one warp, eight rows to a
-// block and no barrier; longer rows take a block of ceil(columns / 1024) warps.
+// each of VPT steps, all asked for before the first is used.  Rows up to 1024
+// columns take one warp, eight rows to a block and no barrier; longer rows take
+// a block of ceil(columns / 1024) warps (512 backward).
+// 131072 rows of 7168 columns to 8 bits: 920 us, 7.2 TB/s; to bf16: 1053 us,
+// 7.1 TB/s; 50021 rows of 2048 columns, bf16: 120 us, 6.8 TB/s, and backward
+// 145 us, 5.7 TB/s.
 #include "ep_ops.cuh"
 
 namespace {

@@ -8,7 +8,8 @@
 // under way that one's search hides behind the others' copies (a block a row
 // left 8 rows to an SM and took 3.4 times as long at 2048 columns), and 32
 // lanes probe 32 rows at a time, so that 3 or 4 loads find a place where
-// halving takes 17.
+// halving takes 17.  358689 rows of 2048 columns from 393216 places: 530 us, 5.9
+// TB/s; 29886 rows of 7168 from 32768: 164 us, 5.5 TB/s.
 #include "ep_ops.cuh"
 
 namespace {

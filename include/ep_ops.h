@@ -124,7 +124,8 @@ ep_status ep_route_backward(int64_t tokens, int32_t experts, int32_t topk, const
  *   y[p, n] = sum_k a[row(p), k] * w[e, n, k],  row(p) = rows[p], or p without rows
  * of 8-bit rows and 8-bit matrices: each block of 128 columns is multiplied on
  * the tensor cores and added to fp32 sums with its two scales.
- *  values, scales: 8-bit rows [a_rows, width]; value_stride a multiple of 16.
+ *  values, scales: 8-bit rows [a_rows, width]; value_stride a multiple of 16
+ *          below 2^31.
  *  w:        e4m3 [experts, gated ? 2 : 1, out, width], dense, 16-byte aligned.
  *  w_scales: fp32 [experts, gated ? 2 : 1, ceil(out/128), ceil(width/128)], dense.
  *  width: a multiple of 16, 16..65536; out: a multiple of 8, 8..65536; experts 1..4096.

@@ -615,3 +615,75 @@ def test_packed_rows_travel_as_one_piece(ep):
         b = ep.Fp8Rows.from_packed(a.packed.clone(), width)
         assert torch.equal(b.values.float(), a.values.float()) and torch.equal(b.scales, a.scales)
         assert torch.equal(b.float(), a.float())
+
+
+# ------------------------------------------------- rows that lie far apart
+def test_norm_offsets_past_32_bits(ep):
+    """Rows 2^27 bytes apart: the last ones lie beyond 2^32 bytes."""
+    g = gen(71)
+    far = torch.empty(36, 1 << 26, dtype=BF, device="cuda")
+    x = far[:, :264]
+    x.copy_(rnd(g, 36, 264))
+    w = rnd(g, 264)
+    y, h, r = R.norm(x, w)
+    near(ep.rms_norm(x, w).out, y, y.abs() * (HALF_BF + 60 * U))
+    n = ep.rms_norm(x.contiguous(), w, out=far[:, 512:776], save_rstd=True)
+    assert torch.equal(n.out, ep.rms_norm(x, w).out)
+    dx, dw = ep.rms_norm_backward(x, x, w, n.rstd, dx=far[:, 1024:1288])
+    dx2, dw2 = ep.rms_norm_backward(x.contiguous(), x.contiguous(), w, n.rstd)
+    assert torch.equal(dx, dx2) and torch.equal(dw, dw2)
+
+
+@pytest.mark.parametrize("gather", [False, True])
+@pytest.mark.parametrize("gated", [False, True])
+def test_product_offsets_past_32_bits(ep, gather, gated):
+    g = gen(72)
+    far = torch.empty(36, 1 << 27, dtype=torch.uint8, device="cuda").view(F8)
+    a = ep.Fp8Rows(far[:, :256], far.view(torch.float32)[:, 256:258])
+    a.values.copy_(rnd(g, 36, 256) * 50)
+    a.scales.copy_(torch.rand(36, 2, device="cuda", generator=g))
+    w, s = weights8(g, *((2, 2, 72, 256) if gated else (2, 72, 256)))
+    off, count, M = places([17, 19])
+    rows = torch.arange(35, -1, -1, dtype=torch.int32, device="cuda") if gather else None
+    out = ep.Fp8Rows(far[:, 4096:4168], far.view(torch.float32)[:, 2048:2049]) if gated else \
+        far.view(BF)[:, 4096:4168]
+    check_product(ep, a, w, s, off, count, rows, out=out)
+
+
+def test_pick_sum_and_route_offsets_past_32_bits(ep):
+    g = gen(73)
+    far = torch.empty(48, 1 << 26, dtype=BF, device="cuda")
+    layer, r, lay, xl = receive_view(ep, 2, 8, 8, 3, g)
+    y = far[:, :72]
+    y.copy_(rnd(g, 48, 72))
+    args = [xl.recv_topk_idx, xl.recv_topk_weights, lay.recv_base, lay.expert_off, xl.expert_count, xl.expert_rows]
+    out = far[:lay.n_recv, 128:200]
+    ep.pick_sum(y, *args, out=out)
+    assert torch.equal(out, ep.pick_sum(y.contiguous(), *args))
+    layer.close()
+    logits = far.view(torch.float32)[:, 1024:1040]
+    logits.copy_(rnd(g, 48, 16))
+    got, _ = check_route(ep, logits, 3, True, None, 1.0)
+    dw = rnd(g, 48, 3)
+    into = far.view(torch.float32)[:, 2048:2064]
+    assert torch.equal(ep.route_backward(logits, got, dw, dlogits=into), ep.route_backward(logits.contiguous(), got, dw))
+
+
+def test_product_at_an_odd_address_of_scales_and_rows(ep):
+    """Scales that start anywhere on 4 bytes, values on 16, outputs on 8 or 16."""
+    g = gen(74)
+    for K in (128, 640, 656):
+        kb = -(-K // 128)
+        base = torch.zeros(70, K + 48, dtype=torch.uint8, device="cuda")
+        a = ep.Fp8Rows(base.view(F8)[:, 16:16 + K], torch.rand(70, kb + 3, device="cuda", generator=g)[:, 1:1 + kb])
+        a.values.copy_(rnd(g, 70, K) * 30)
+        off, count, M = places([30, 40])
+        w, s = weights8(g, 2, 2, 136, K)
+        buf = torch.zeros(70, 160, dtype=torch.uint8, device="cuda")
+        out = ep.Fp8Rows(buf.view(F8)[:, 8:144], torch.zeros(70, 5, device="cuda")[:, 1:3])
+        check_product(ep, a, w, s, off, count, out=out)
+        assert (buf[:, :8] == 0).all() and (buf[:, 144:] == 0).all()
+        w, s = weights8(g, 2, 136, K)
+        wide = torch.zeros(70, 168, dtype=BF, device="cuda")
+        check_product(ep, a, w, s, off, count, out=wide[:, 8:144])
+        assert (wide[:, :8] == 0).all() and (wide[:, 144:] == 0).all()
