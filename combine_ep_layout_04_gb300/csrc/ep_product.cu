@@ -9,7 +9,7 @@
 // accumulators' way round -- products, sums, products again -- bounds the
 // kernel rather than the tensor cores: loads and products alone run at 3.4
 // PFLOP/s, with the sums at 2.7 (32768 places, 7168 columns, 4096 matrix rows:
-// 720 us; gated, 2 x 2048 rows: 700 us, 835 us with the rows gathered; 2048
+// 720 us; gated, 2 x 2048 rows: 705 us, 820 us with the rows gathered; 2048
 // columns, 7168 rows: 438 us, where each tile's 16 blocks leave more of its
 // stores in sight).  With few places to an expert the matrices' bytes count:
 // 61 places on 32 experts of 7168 x 2048 take 79 us, 5 TB/s.
@@ -23,7 +23,7 @@
 //    rows takes 80 cycles, twice as much time as the block's products);
 //  - products, one thread of the first CTA, into four accumulators of 128
 //    columns;
-//  - scales, one warp: the row scales of 128 places are 128 lines of memory, so
+//  - scales, two warps: the row scales of 128 places are 128 lines of memory, so
 //    they are fetched four blocks at a time, well ahead;
 //  - sums, eight warps of 128 fp32 sums a thread.
 #include <cuda.h>
@@ -74,13 +74,16 @@ constexpr int kGatherWarps = 4;        // warps that fetch rows one by one, wher
 constexpr int kGatherRows = kRows / (kGatherWarps * 4);      // rows a gathering thread has a part of
 constexpr int kGatherLag = 3;          // blocks of 128 columns a gathering thread has in flight
 constexpr int threads_of(bool gather) { return 32 * (4 + kSums + (gather ? kGatherWarps : 0)); }
+constexpr int kScaleWarps = 2;         // warps that fetch the rows' scales
 // Registers: a sums thread holds 128 fp32 sums; the other warpgroups give up
-// what they do not need.  The shares stay within the launch's.
-constexpr int kLoadRegs = 104, kGatherRegs = 56;
-constexpr int sum_regs(bool gather) { return gather ? 176 : 200; }
+// what they do not need, and the shares stay within the launch's.  At 176 the
+// sums of 32768 places took 735 us for 700 (gated, 7168 columns); a share in
+// which anything spills costs a quarter.
+constexpr int load_regs(bool gather) { return gather ? 64 : 72; }
+constexpr int kGatherRegs = 48, kSumRegs = 200;
 constexpr int launch_regs(bool gather) { return 65536 / threads_of(gather) / 8 * 8; }
-static_assert(128 * kLoadRegs + 256 * sum_regs(false) <= threads_of(false) * launch_regs(false) &&
-              128 * (kLoadRegs + kGatherRegs) + 256 * sum_regs(true) <= threads_of(true) * launch_regs(true),
+static_assert(128 * load_regs(false) + 256 * kSumRegs <= threads_of(false) * launch_regs(false) &&
+                  128 * (load_regs(true) + kGatherRegs) + 256 * kSumRegs <= threads_of(true) * launch_regs(true),
               "register shares exceed the launch's");
 // Scales of the blocks under way, by step.  A slot is written again 16 steps
 // later, when the stage of 10 steps later has been multiplied, which took the
@@ -291,7 +294,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(kGather),
 
     if (tid == 0) {
         for (int i = 0; i < kStages; ++i)
-            mbar_init(&bar.full[i], 3 + (kGather ? 2 * kGatherWarps : 0)), mbar_init(&bar.empty[i], 1);
+            mbar_init(&bar.full[i], 1 + 2 * kScaleWarps + (kGather ? 2 * kGatherWarps : 0)), mbar_init(&bar.empty[i], 1);
         for (int i = 0; i < 4; ++i) mbar_init(&bar.tfull[i], 1), mbar_init(&bar.tempty[i], kSums);
         for (int i = 0; i < 4; ++i) mbar_init(&bar.pair[i], 2);
         mbar_fence_init();
@@ -334,7 +337,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(kGather),
     fence_after();
     const uint32_t tmem = s_tmem;
     if (warp < 4) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLoadRegs));
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(load_regs(kGather)));
         int stage = 0;
         uint32_t phase = 0;
         if (warp == 0) {
@@ -395,17 +398,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(kGather),
                 }
             }
             __syncwarp();
-        } else if (warp == 2) {
-            // ---- scales, which come four blocks ahead: of four rows a lane, and of the tile's two matrix
-            // blocks, one block of 128 columns to each of eight lanes
+        } else {
+            // ---- scales, which come four blocks ahead: of two rows a lane; and, by the first of the two
+            // warps, of the tile's two matrix blocks, one block of 128 columns to each of eight lanes
+            constexpr int kEach = kRows / 32 / kScaleWarps;
+            const int part = warp - 2;
             int slot = 0;
             for (int id = cluster;; id += clusters) {
                 const Tile t = tile_of(p, start, rank, id);
                 if (!t.any) break;
-                const float *sa[4];
+                const float *sa[kEach];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int row = j * 32 + lane;
+                for (int j = 0; j < kEach; ++j) {
+                    const int row = (part * kEach + j) * 32 + lane;
                     sa[j] = nullptr;
                     if (row < t.here) {
                         const int src = kGather ? p.rows[t.first + row] : t.first + row;
@@ -417,10 +422,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(kGather),
                 const float *sw = p.w_scales + (lane & 3) +
                                   ((static_cast<int64_t>(t.expert) * (kGated ? 2 : 1) + (kGated ? (lane >> 2) & 1 : 0)) * p.nb +
                                    min(block, p.nb - 1)) * p.kb;
-                float x[4][4], w = 0.0f;
+                float x[kEach][4], w = 0.0f;
                 auto scales = [&](int kb) {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
+                    for (int j = 0; j < kEach; ++j) {
                         x[j][0] = x[j][1] = x[j][2] = x[j][3] = 0.0f;
                         if (!sa[j]) continue;
                         if (p.wide_scales && kb + 4 <= p.kb) {
@@ -432,14 +437,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(kGather),
                                 if (kb + i < p.kb) x[j][i] = sa[j][kb + i];
                         }
                     }
-                    if (lane < 8 && kb + (lane & 3) < p.kb) w = sw[kb];
+                    if (part == 0 && lane < 8 && kb + (lane & 3) < p.kb) w = sw[kb];
                 };
                 scales(0);
                 for (int k0 = 0; k0 < p.kb; k0 += 4) {
-                    float xs[4][4];
+                    float xs[kEach][4];
                     const float ws = w;
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
+                    for (int j = 0; j < kEach; ++j)
 #pragma unroll
                         for (int i = 0; i < 4; ++i) xs[j][i] = x[j][i];
                     scales(k0 + 4);
@@ -448,9 +453,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(kGather),
                         if (k0 + i >= p.kb) break;
                         if (!wait_for(&bar.empty[stage], phase ^ 1u, &s_stop)) goto done;
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) s_x[slot][j * 32 + lane] = xs[j][i];
-                        if (lane < 8 && (lane & 3) == i) s_w[slot][lane >> 2] = ws;
-                        if (k0 + i == 0 && lane == 0) s_tile[slot][0] = t.first, s_tile[slot][1] = t.here, s_tile[slot][2] = t.n;
+                        for (int j = 0; j < kEach; ++j) s_x[slot][(part * kEach + j) * 32 + lane] = xs[j][i];
+                        if (part == 0 && lane < 8 && (lane & 3) == i) s_w[slot][lane >> 2] = ws;
+                        if (part == 0 && k0 + i == 0 && lane == 0) s_tile[slot][0] = t.first, s_tile[slot][1] = t.here, s_tile[slot][2] = t.n;
                         __syncwarp();
                         // the sums learn of it by way of the step's products (a barrier of their own for
                         // it made a step of 0.51 us take 0.56)
@@ -514,7 +519,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(kGather),
             if (++late == kStages) late = 0;
         }
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(sum_regs(kGather)));
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSumRegs));
         // ---- sums: accumulator times the two scales, added up in registers.
         // A warp reads the 32 rows that its number allows, and one half's
         // accumulators: a block of 128 columns, or 64 of the gate's and the same 64
