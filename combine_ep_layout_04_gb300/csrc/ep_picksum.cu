@@ -4,12 +4,12 @@
 //
 // Bound by memory: every place's row is read once, every receive row written
 // once.  A pick's place is found by searching its expert's rows, which are in
-// increasing order.  A warp takes up to 2048 columns of a row: enough warps are
+// increasing order.  A warp takes up to 4096 columns of a row: enough warps are
 // under way that one's search hides behind the others' copies (a block a row
 // left 8 rows to an SM and took 3.4 times as long at 2048 columns), and 32
 // lanes probe 32 rows at a time, so that 3 or 4 loads find a place where
-// halving takes 17.  358689 rows of 2048 columns from 393216 places: 530 us, 5.9
-// TB/s; 29886 rows of 7168 from 32768: 164 us, 5.5 TB/s.
+// halving takes 17.  29886 rows of 7168 columns from 32768 places: 149 us, 6.1
+// TB/s; 358689 rows of 2048 from 393216: 490 us, 6.3 TB/s.
 #include "ep_ops.cuh"
 
 namespace {
@@ -17,8 +17,11 @@ namespace {
 using namespace ep;
 
 constexpr int kWarps = 8;          // a block's
-constexpr int kPartVecs = 256;     // most 16-byte vectors of a row's part
-constexpr int kAtOnce = 4;         // vectors a lane has under way
+constexpr int kPartVecs = 512;     // most 16-byte vectors of a row's part
+// Vectors a lane has under way, and blocks to an SM: two by six (40 registers)
+// took 149 and 490 us in the cases above, four by four 147 and 503, four by
+// three 163 and 525, one by eight 167 and 520.
+constexpr int kAtOnce = 2, kBlocks = 6;
 
 struct SumParams {
     int64_t rows, places;
@@ -48,7 +51,7 @@ __device__ __forceinline__ int find_place(const SumParams &p, int e, int r, int 
     return p.expert_rows[lo] == r ? static_cast<int>(lo) : -1;
 }
 
-__global__ void __launch_bounds__(32 * kWarps) pick_sum_kernel(SumParams p) {
+__global__ void __launch_bounds__(32 * kWarps, kBlocks) pick_sum_kernel(SumParams p) {
     const int lane = threadIdx.x & 31;
     const int64_t item = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
     const int64_t r = item / p.parts;

@@ -77,16 +77,24 @@ class Fp8Rows:
         self._buffer, self._width = buffer, width
         return self
 
+    def _split(self) -> None:
+        """Makes the views of a packed buffer (one call for both: they cost as much as a small kernel)."""
+        at, blocks = _scales_at(self._width), _blocks(self._width)
+        values, scales = self._buffer.split_with_sizes((at, self._buffer.shape[1] - at), 1)
+        scales = scales.view(_F32)
+        self._values = values if at == self._width else values.narrow(1, 0, self._width)
+        self._scales = scales if scales.shape[1] == blocks else scales.narrow(1, 0, blocks)
+
     @property
     def values(self) -> torch.Tensor:
         if self._values is None:
-            self._values = self._buffer.narrow(1, 0, self._width)
+            self._split()
         return self._values
 
     @property
     def scales(self) -> torch.Tensor:
         if self._scales is None:
-            self._scales = self._buffer.view(_F32).narrow(1, _scales_at(self._width) // 4, _blocks(self._width))
+            self._split()
         return self._scales
 
     @property
