@@ -745,7 +745,7 @@ extern "C" ep_status ep_expert_product(int64_t places, int64_t a_rows, int32_t e
         return EP_ERR_INVALID_ARG;
     const Caller c;
     if (!c.ok) return EP_ERR_CUDA;
-    if (!c.has_or_null(values) || !c.has_or_null(scales) || !c.has(w) || !c.has(w_scales) || !c.has(expert_off) ||
+    if ((a_rows > 0 && (!c.has(values) || !c.has(scales))) || !c.has(w) || !c.has(w_scales) || !c.has(expert_off) ||
         !c.has(expert_count) || !c.has_or_null(rows) || !c.has_or_null(out_bf16) || !c.has_or_null(out_values) ||
         !c.has_or_null(out_scales) || !c.has_or_null(status))
         return EP_ERR_INVALID_ARG;

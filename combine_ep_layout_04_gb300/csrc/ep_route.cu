@@ -467,7 +467,8 @@ __global__ void __launch_bounds__(32 * kWarps, VPT <= 8 ? 4 : 1) route_grad_kern
             if (e < E) {
                 float d[V];
 #pragma unroll
-                for (int i = 0; i < V; ++i) d[i] = l[j + i] * (g[j + i] - inner) + (p.renormalize ? picks[e + i] : 0.0f);
+                for (int i = 0; i < V; ++i)
+                    d[i] = (live ? l[j + i] * (g[j + i] - inner) : 0.0f) + (p.renormalize ? picks[e + i] : 0.0f);
                 if (p.bf16) {
                     __nv_bfloat16 *to = static_cast<__nv_bfloat16 *>(p.dlogits) + t * p.dlogits_stride + e;
                     if constexpr (V == 4) *reinterpret_cast<uint2 *>(to) = make_uint2(pack2(d[0], d[1]), pack2(d[2], d[3]));

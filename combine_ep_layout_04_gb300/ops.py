@@ -207,6 +207,8 @@ def _fp8_rows(r, name: str, index: int, shape, align: int) -> tuple[int, int, in
     buffer = r._buffer
     if buffer is not None and r._width == shape[1] and buffer.shape[0] == shape[0] and buffer.get_device() == index:
         ptr, stride = buffer.data_ptr(), buffer.shape[1]
+        if not shape[0]:
+            return 0, stride, 0, stride // 4
         if not ptr & 15:
             return ptr, stride, ptr + _scales_at(shape[1]), stride // 4
     pv, sv = _rows(r.values, name + ".values", _FP8, index, shape, align)

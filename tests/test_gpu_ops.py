@@ -687,3 +687,58 @@ def test_product_at_an_odd_address_of_scales_and_rows(ep):
         wide = torch.zeros(70, 168, dtype=BF, device="cuda")
         check_product(ep, a, w, s, off, count, out=wide[:, 8:144])
         assert (wide[:, :8] == 0).all() and (wide[:, 144:] == 0).all()
+
+
+def test_route_backward_leaves_padded_tokens_zero_whatever_the_loss(ep):
+    g = gen(81)
+    logits = rnd(g, 40, 64)
+    mask = torch.arange(40, device="cuda") % 4 != 0
+    logits[5] = R.NEG
+    for renorm in (True, False):
+        r = ep.route(logits, 4, renormalize=renorm, token_mask=mask, balance_coef=1.0)
+        d = ep.route_backward(logits, r, torch.full((40, 4), float("nan"), device="cuda"),
+                              torch.tensor(float("nan"), device="cuda"))
+        assert (d[~mask] == 0).all() and (d[5] == 0).all()
+        assert d[mask].isnan().any(1).sum() == mask.sum() - 1
+
+
+@pytest.mark.parametrize("E,N,K,M", [(4096, 8, 16, 5000), (700, 72, 144, 300), (1, 8, 65536, 3), (1, 65536, 16, 5),
+                                     (3, 16, 16384, 400)])
+@pytest.mark.parametrize("gated", [False, True])
+def test_product_at_its_largest_sizes(ep, E, N, K, M, gated):
+    g = gen(E + N)
+    count = torch.bincount(torch.randint(E, (M,), device="cuda", generator=g), minlength=E)
+    off = count.cumsum(0) - count
+    w, s = weights8(g, *((E, 2, N, K) if gated else (E, N, K)))
+    check_product(ep, rows8(g, ep, M, K), w, s, off.int(), count.int())
+
+
+@pytest.mark.parametrize("gated", [False, True])
+def test_product_of_rows_that_are_not_there(ep, gated):
+    """Without any row to read every place is zeros, and said so."""
+    g = gen(83)
+    w, s = weights8(g, *((2, 2, 64, 128) if gated else (2, 64, 128)))
+    off, count, M = places([30, 4])
+    rows = torch.zeros(M, dtype=torch.int32, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    y = ep.expert_product(ep.Fp8Rows.empty(0, 128), w, s, off, count, rows=rows, status=status)
+    assert status.item() == 1 and ((y.values.float() if gated else y) == 0).all()
+    status.zero_()
+    ep.expert_product(ep.Fp8Rows.empty(0, 128), w, s, off, torch.zeros_like(count), rows=rows, status=status)
+    assert status.item() == 0
+
+
+def test_pick_sum_with_long_segments(ep):
+    """A rank's only expert lists every row: the search takes several rounds and ends on any of them."""
+    g = gen(84)
+    for T in (31, 32, 33, 1023, 1025, 40000):
+        layer, r, lay, xl = receive_view(ep, 1, T, 2, 2, g)
+        y = rnd(g, xl.expert_rows.shape[0], 8, dtype=BF)
+        got = ep.pick_sum(y, xl.recv_topk_idx, xl.recv_topk_weights, lay.recv_base, lay.expert_off, xl.expert_count,
+                          xl.expert_rows)
+        # both experts list every row in order
+        w = xl.recv_topk_weights.double()
+        at = xl.recv_topk_idx.long() * T + torch.arange(T, device="cuda")[:, None]
+        want = (w[..., None] * y[at].double()).sum(1)
+        near(got, want, want.abs() * HALF_BF + (w[..., None] * y[at].double()).abs().sum(1) * 3 * U)
+        layer.close()
