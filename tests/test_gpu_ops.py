@@ -328,6 +328,14 @@ def test_product_many_places_to_an_expert(ep, counts, N, K, gated, gather):
     test_product(ep, counts, N, K, gated, gather)
 
 
+@pytest.mark.parametrize("counts", [[130] + [0] * 9, [0, 65, 1, 33, 0, 0, 0, 0, 64, 0, 2, 32], [3] * 20, [16]])
+@pytest.mark.parametrize("N,K", [(8, 16), (136, 144), (264, 400), (512, 1024)])
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("gather", [False, True])
+def test_product_few_places_to_an_expert(ep, counts, N, K, gated, gather):
+    test_product(ep, counts, N, K, gated, gather)
+
+
 @pytest.mark.parametrize("gated", [False, True])
 def test_product_long_rows_many_experts(ep, gated):
     g = gen(31)
