@@ -2,21 +2,22 @@
 // their weights, per-expert counts and the balance loss, and the logits'
 // gradient (include/ep_ops.h).
 //
-// A warp holds a token's logits in registers, VPT to a lane, in vectors of V
-// neighbouring experts (V = 1 where a row's address or E does not allow more).
+// A warp, or half a warp (L lanes: half for up to 256 experts and 8 picks), holds
+// a token's logits in registers, VPT to a lane, in vectors of V neighbouring
+// experts (V = 1 where a row's address or E does not allow more).
 // The K largest are found without sorting:
-//  - the largest logit of each pair of lanes is known (of each lane for K > 16),
-//    and the K-th largest of these, from a bitonic sort across the lanes, is a
-//    bound that at least K logits reach (K warp-wide maxima in its place cost
-//    a third of the kernel);
+//  - the largest logit of each lane is known (of each pair of lanes in a whole
+//    warp with up to 16 picks), and the K-th largest of these, from a bitonic
+//    sort across the lanes, is a bound that at least K logits reach (K
+//    warp-wide maxima in its place cost a third of the kernel);
 //  - the few logits that reach it -- about K + 3 of 256 -- are listed in shared
 //    memory as 64-bit words, the logit's bits in the floats' order and then the
 //    expert, so that ties go to the lower one;
 //  - each of them counts the words above its own: that is its place.
-// Bound by issue, not memory: about 450 instructions a token and warp, where K
-// rounds of a maximum over all logits took 1800 (131072 tokens of 256 fp32
-// logits, top 8: 67 us against 207; with the loss and counts 96 us; the
-// gradient, bound by memory more than by issue, 52 us, 5.4 TB/s).
+// Bound by issue, not memory; K rounds of a maximum over all logits took 1800
+// instructions a token (131072 tokens of 256 fp32 logits, top 8: 47 us against
+// 207; with the loss and counts 75 us; the gradient, bound by memory more than
+// by issue, 54 us, 5.0 TB/s).
 #include <type_traits>
 
 #include "ep_ops.cuh"
@@ -52,26 +53,33 @@ __device__ __forceinline__ float key_value(uint32_t k) {
     return __uint_as_float((k & 0x80000000u) ? k & 0x7fffffffu : ~k);
 }
 
-constexpr int kWords = 64;         // words of a warp's list, two a lane; a longer one (ties, wide K) takes the slow way
-static_assert(kWords * sizeof(int) <= kMaxTopk * sizeof(unsigned long long), "the list's experts share the picks' room");
+// A token's list has two words to a lane; a longer one (ties, wide K) takes the
+// slow way.  The list's experts share the picks' room, one word to a lane.
 
 __device__ __forceinline__ unsigned long long pick_word(float l, int e) {
     return (static_cast<unsigned long long>(order_key(l)) << 32) | static_cast<uint32_t>(~e);
 }
 
-// The expert of a lane's j-th logit.
-template <int V>
+// The expert of the j-th logit of lane `lane` of L.
+template <int L, int V>
 __device__ __forceinline__ int expert_of(int j, int lane) {
-    return (j / V) * 32 * V + lane * V + j % V;
+    return (j / V) * L * V + lane * V + j % V;
+}
+// Sum over the L lanes of a token.
+template <int L>
+__device__ __forceinline__ float lanes_sum(float v) {
+#pragma unroll
+    for (int o = L / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
 }
 
 // Loads a lane's logits; what lies past the experts is -inf.  For V > 1 the
 // experts and the row's address are multiples of V.
-template <int VPT, int V>
+template <int L, int VPT, int V>
 __device__ __forceinline__ void load_row(const void *logits, int bf16, int64_t at, int experts, int lane, float (&l)[VPT]) {
 #pragma unroll
     for (int j = 0; j < VPT; j += V) {
-        const int e = expert_of<V>(j, lane);
+        const int e = expert_of<L, V>(j, lane);
         if (e >= experts) {
 #pragma unroll
             for (int i = 0; i < V; ++i) l[j + i] = -INFINITY;
@@ -101,39 +109,43 @@ __device__ __forceinline__ void load_row(const void *logits, int bf16, int64_t a
     }
 }
 
-// Sorts a value of each lane across the warp, largest first, by exchanges over
-// distances from kPair up (kPair = 2: lanes of a pair hold the same value).
-template <int kPair>
+// Sorts a value of each of L lanes, largest first, by exchanges over distances
+// from kPair up (kPair = 2: lanes of a pair hold the same value).
+template <int L, int kPair>
 __device__ __forceinline__ float sort_lanes(float v, int lane) {
 #pragma unroll
-    for (int k = 2 * kPair; k <= 32; k *= 2)
+    for (int k = 2 * kPair; k <= L; k *= 2)
 #pragma unroll
         for (int j = k / 2; j >= kPair; j /= 2) {
             const float o = __shfl_xor_sync(0xffffffffu, v, j);
-            const bool larger = ((lane & j) == 0) == ((lane & k) == 0 || k == 32);
+            const bool larger = ((lane & j) == 0) == ((lane & k) == 0 || k == L);
             v = larger ? fmaxf(v, o) : fminf(v, o);
         }
     return v;
 }
 
-// Lane k gets pick k's word, 0 where there is none; top: the largest logit, or
-// -inf if none is above it.  row: the warp's room for the logits.
-template <int VPT, int V>
+// Lane k of a token's gets pick k's word, 0 where there is none; top: the
+// largest logit, or -inf if none is above it.  row: room for the logits; lane:
+// of the token's L.  All 32 lanes come here together.
+template <int L, int VPT, int V>
 __device__ __forceinline__ unsigned long long pick(const float (&l)[VPT], int E, int K, int lane, float *row,
                                                    unsigned long long *words, unsigned long long *picks, float &top) {
+    constexpr int kWords = 2 * L;
+    const int shift = L == 32 ? 0 : threadIdx.x & 16;      // where the token's lanes are in a ballot
+    const uint32_t below = (1u << lane) - 1u;
     float most = l[0];
 #pragma unroll
     for (int j = 1; j < VPT; ++j) most = fmaxf(most, l[j]);      // NaN is passed over
     most = most > -INFINITY ? most : -INFINITY;
     float bound;
-    if (K <= 16) {
-        most = sort_lanes<2>(fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1)), lane);
-        bound = __shfl_sync(0xffffffffu, most, 2 * (K - 1));
+    if (L == 32 && K <= 16) {
+        most = sort_lanes<L, 2>(fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1)), lane);
+        bound = __shfl_sync(0xffffffffu, most, 2 * (K - 1), L);
     } else {
-        most = sort_lanes<1>(most, lane);
-        bound = __shfl_sync(0xffffffffu, most, K - 1);
+        most = sort_lanes<L, 1>(most, lane);
+        bound = __shfl_sync(0xffffffffu, most, K - 1, L);
     }
-    top = __shfl_sync(0xffffffffu, most, 0);
+    top = __shfl_sync(0xffffffffu, most, 0, L);
     // fewer than K of them: every logit above -inf is on the list
     const float least = bound > -INFINITY ? bound : -3.402823466e38f;
     // the logits where any lane can read them, and the experts on the list: a
@@ -141,7 +153,7 @@ __device__ __forceinline__ unsigned long long pick(const float (&l)[VPT], int E,
     // have none)
 #pragma unroll
     for (int j = 0; j < VPT; j += V) {
-        const int e = expert_of<V>(j, lane);
+        const int e = expert_of<L, V>(j, lane);
         if (e < E) {
             if constexpr (V == 4) *reinterpret_cast<float4 *>(row + e) = make_float4(l[j], l[j + 1], l[j + 2], l[j + 3]);
             else if constexpr (V == 2) *reinterpret_cast<float2 *>(row + e) = make_float2(l[j], l[j + 1]);
@@ -155,9 +167,10 @@ __device__ __forceinline__ unsigned long long pick(const float (&l)[VPT], int E,
         uint32_t on = 0;
 #pragma unroll
         for (int j = j0; j < VPT && j < j0 + 32; ++j) on |= l[j] >= least ? 1u << (j - j0) : 0u;
-        for (uint32_t lanes = __ballot_sync(0xffffffffu, on != 0); lanes; lanes = __ballot_sync(0xffffffffu, on != 0)) {
-            const int j = j0 + __ffs(on) - 1, at = n + __popc(lanes & ((1u << lane) - 1u));
-            if (on && at < kWords) experts[at] = expert_of<V>(j, lane);
+        for (uint32_t any = __ballot_sync(0xffffffffu, on != 0); any; any = __ballot_sync(0xffffffffu, on != 0)) {
+            const uint32_t lanes = L == 32 ? any : any >> shift & 0xffffu;
+            const int j = j0 + __ffs(on) - 1, at = n + __popc(lanes & below);
+            if (on && at < kWords) experts[at] = expert_of<L, V>(j, lane);
             on &= on - 1;
             n += __popc(lanes);
         }
@@ -166,62 +179,68 @@ __device__ __forceinline__ unsigned long long pick(const float (&l)[VPT], int E,
     const int listed = n <= kWords ? n : 0;
     unsigned long long a = 0, b = 0;
     if (lane < listed) a = pick_word(row[experts[lane]], experts[lane]);
-    if (lane + 32 < listed) b = pick_word(row[experts[lane + 32]], experts[lane + 32]);
+    if (lane + L < listed) b = pick_word(row[experts[lane + L]], experts[lane + L]);
     __syncwarp();
     words[lane] = a;                     // the list ends in zeros
-    words[lane + 32] = b;
+    words[lane + L] = b;
     __syncwarp();
-    unsigned long long mine = 0;
-    if (n <= kWords) {
-        int above_a = 0, above_b = 0;
-        for (int q = 0; q < n; q += 4) {
-            const ulonglong2 u = *reinterpret_cast<const ulonglong2 *>(words + q);
-            const ulonglong2 v = *reinterpret_cast<const ulonglong2 *>(words + q + 2);
-            const unsigned long long w[4] = {u.x, u.y, v.x, v.y};
+    // the longer list of the two tokens of a warp
+    const int longest = L == 32 ? listed : max(listed, __shfl_xor_sync(0xffffffffu, listed, 16));
+    int above_a = 0, above_b = 0;
+    for (int q = 0; q < longest; q += 4) {
+        const ulonglong2 u = *reinterpret_cast<const ulonglong2 *>(words + q);
+        const ulonglong2 v = *reinterpret_cast<const ulonglong2 *>(words + q + 2);
+        const unsigned long long w[4] = {u.x, u.y, v.x, v.y};
 #pragma unroll
-            for (int i = 0; i < 4; ++i) above_a += w[i] > a;
-            if (n > 32) {
+        for (int i = 0; i < 4; ++i) above_a += w[i] > a;
+        if (longest > L) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) above_b += w[i] > b;
-            }
+            for (int i = 0; i < 4; ++i) above_b += w[i] > b;
         }
-        if (a && above_a < K) picks[above_a] = a;
-        if (b && above_b < K) picks[above_b] = b;
-        __syncwarp();
-        if (lane < K && lane < n) mine = picks[lane];
-        __syncwarp();
-    } else {
+    }
+    if (a && above_a < K) picks[above_a] = a;
+    if (b && above_b < K) picks[above_b] = b;
+    __syncwarp();
+    unsigned long long mine = lane < K && lane < listed ? picks[lane] : 0;
+    __syncwarp();
+    if (__any_sync(0xffffffffu, n > kWords)) {
         // one pick after another: the largest word below the last pick
         unsigned long long last = ~0ull;
         for (int k = 0; k < K; ++k) {
             unsigned long long best = 0;
 #pragma unroll
             for (int j = 0; j < VPT; ++j) {
-                const unsigned long long w = l[j] > -INFINITY ? pick_word(l[j], expert_of<V>(j, lane)) : 0;
+                const unsigned long long w = l[j] > -INFINITY ? pick_word(l[j], expert_of<L, V>(j, lane)) : 0;
                 if (w < last && w > best) best = w;
             }
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) {
+            for (int o = L / 2; o > 0; o >>= 1) {
                 const unsigned long long w = __shfl_xor_sync(0xffffffffu, best, o);
                 best = w > best ? w : best;
             }
-            if (best == 0) break;
-            if (lane == k) mine = best;
+            if (lane == k && n > kWords) mine = best;
             last = best;
         }
     }
     return mine;
 }
 
-template <int VPT, int V, bool kTrain>
-__global__ void __launch_bounds__(32 * kWarps, VPT <= 8 ? 4 : 1) route_kernel(RouteParams p) {
-    // a row of logits, in the end of p sums, for each warp [kWarps][experts up to a multiple of 4]; kTrain: then
+// Blocks that run on an SM at once, by the registers a lane's logits take.  For
+// 16 to a lane the router has three and its gradient two: 131072 tokens of 256
+// logits take 47 against 54 us, and 54 against 71.
+constexpr int route_on_sm(int vpt) { return vpt <= 8 ? 4 : vpt <= 16 ? 3 : 1; }
+constexpr int grad_on_sm(int vpt) { return vpt <= 8 ? 4 : vpt <= 16 ? 2 : 1; }
+
+template <int L, int VPT, int V, bool kTrain>
+__global__ void __launch_bounds__(32 * kWarps, route_on_sm(VPT)) route_kernel(RouteParams p) {
+    constexpr int kTeams = kWarps * 32 / L;      // tokens a block works on at once
+    // a row of logits, in the end of p sums, for each of them [kTeams][experts up to a multiple of 4]; kTrain: then
     // counts [experts]
     extern __shared__ __align__(16) float smem[];
-    __shared__ __align__(16) unsigned long long s_words[kWarps][kWords], s_picks[kWarps][kMaxTopk];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    __shared__ __align__(16) unsigned long long s_words[kTeams][2 * L], s_picks[kTeams][L];
+    const int team = threadIdx.x / L, lane = threadIdx.x % L;
     const int E = p.experts, K = p.topk, E4 = (E + 3) & ~3;
-    int32_t *count = reinterpret_cast<int32_t *>(smem + kWarps * E4);
+    int32_t *count = reinterpret_cast<int32_t *>(smem + kTeams * E4);
     float psum[kTrain ? VPT : 1];
     int live_tokens = 0;
     if (kTrain) {
@@ -231,34 +250,29 @@ __global__ void __launch_bounds__(32 * kWarps, VPT <= 8 ? 4 : 1) route_kernel(Ro
         for (int j = 0; j < VPT; ++j) psum[j] = 0.0f;
         __syncthreads();
     }
-    const uint32_t T = static_cast<uint32_t>(p.tokens), stride = gridDim.x * kWarps;
-    uint32_t t = blockIdx.x * kWarps + warp;
-    // a token's logits are on their way while the last one's are worked on, where they fit twice
+    const uint32_t T = static_cast<uint32_t>(p.tokens), stride = gridDim.x * kTeams;
+    uint32_t t = blockIdx.x * kTeams + team;
+    // A token's logits are on their way while the last one's are worked on, where they fit twice.
     constexpr bool kAhead = VPT <= 16;
     float ahead[kAhead ? VPT : 1];
-    bool live_ahead = false;
-    if (kAhead && t < T) {
-        live_ahead = p.mask == nullptr || p.mask[t] != 0;
-        if constexpr (kAhead) load_row<VPT, V>(p.logits, p.bf16, t * p.logits_stride, live_ahead ? E : 0, lane, ahead);
-    }
-    for (; t < T; t += stride) {
+    bool live_ahead = t < T && (p.mask == nullptr || p.mask[t] != 0);
+    if constexpr (kAhead) load_row<L, VPT, V>(p.logits, p.bf16, t * p.logits_stride, live_ahead ? E : 0, lane, ahead);
+    // both tokens of a warp go on until the first is past the end; a token past it is a padded one that is not stored
+    for (; t - (L == 32 ? 0 : team & 1) < T; t += stride) {
         float l[VPT];
-        bool live;
+        const bool inside = t < T, live = live_ahead;
         if constexpr (kAhead) {
-            live = live_ahead;
 #pragma unroll
             for (int j = 0; j < VPT; ++j) l[j] = ahead[j];
-            if (t + stride < T) {
-                live_ahead = p.mask == nullptr || p.mask[t + stride] != 0;
-                load_row<VPT, V>(p.logits, p.bf16, (t + stride) * p.logits_stride, live_ahead ? E : 0, lane, ahead);
-            }
         } else {
-            live = p.mask == nullptr || p.mask[t] != 0;
-            load_row<VPT, V>(p.logits, p.bf16, t * p.logits_stride, live ? E : 0, lane, l);
+            load_row<L, VPT, V>(p.logits, p.bf16, t * p.logits_stride, live ? E : 0, lane, l);
         }
+        live_ahead = t + stride < T && (p.mask == nullptr || p.mask[t + stride] != 0);
+        if constexpr (kAhead)
+            load_row<L, VPT, V>(p.logits, p.bf16, (t + stride) * p.logits_stride, live_ahead ? E : 0, lane, ahead);
         live_tokens += live;
         float top;
-        const unsigned long long word = pick<VPT, V>(l, E, K, lane, smem + warp * E4, s_words[warp], s_picks[warp], top);
+        const unsigned long long word = pick<L, VPT, V>(l, E, K, lane, smem + team * E4, s_words[team], s_picks[team], top);
         const int my_e = word ? static_cast<int>(~static_cast<uint32_t>(word)) : -1;
         const float most = top > -INFINITY ? top : 0.0f;
         float sum = 0.0f;
@@ -268,24 +282,25 @@ __global__ void __launch_bounds__(32 * kWarps, VPT <= 8 ? 4 : 1) route_kernel(Ro
                 l[j] = __expf(l[j] - most);
                 sum += l[j];
             }
-            sum = warp_sum(sum);       // 0 if no logit is left, NaN if one is NaN
+            sum = lanes_sum<L>(sum);       // 0 if no logit is left, NaN if one is NaN
         }
         float w = word ? __expf(key_value(static_cast<uint32_t>(word >> 32)) - most) : 0.0f;
-        const float total = p.renormalize ? warp_sum(w) : sum;
+        const float total = p.renormalize ? lanes_sum<L>(w) : sum;
         w = word ? __fdividef(w, total) : 0.0f;      // total is 1 .. experts, or NaN
         const uint64_t at = static_cast<uint64_t>(t) * static_cast<uint32_t>(K) + lane;
-        if (lane < K) {
+        if (lane < K && inside) {
             p.topk_idx[at] = my_e;
             p.topk_weights[at] = w;
         }
         if (p.rank_weights) {
-            const int rank = my_e >= 0 ? my_e / p.per_rank : -1 - lane;
+            const int self = threadIdx.x & 31;
+            const int rank = my_e >= 0 ? my_e / p.per_rank + (self / L << 16) : -1 - self;
             const uint32_t same = __match_any_sync(0xffffffffu, rank);
-            if (lane < K) p.rank_weights[at] = my_e >= 0 && __ffs(same) - 1 == lane ? 1.0f : 0.0f;
+            if (lane < K && inside) p.rank_weights[at] = my_e >= 0 && __ffs(same) - 1 == self ? 1.0f : 0.0f;
         }
         if (kTrain) {
             if (my_e >= 0) atomicAdd(&count[my_e], 1);
-            if (lane == 0) p.lse[t] = live ? (top > -INFINITY ? most + logf(sum) : sum != sum ? sum : -INFINITY) : INFINITY;
+            if (lane == 0 && inside) p.lse[t] = live ? (top > -INFINITY ? most + logf(sum) : sum != sum ? sum : -INFINITY) : INFINITY;
             const float inv = sum != 0.0f ? 1.0f / sum : 0.0f;
 #pragma unroll
             for (int j = 0; j < VPT; ++j) psum[j] = fmaf(l[j], inv, psum[j]);
@@ -294,19 +309,19 @@ __global__ void __launch_bounds__(32 * kWarps, VPT <= 8 ? 4 : 1) route_kernel(Ro
     if (kTrain) {
 #pragma unroll
         for (int j = 0; j < VPT; ++j)
-            if (expert_of<V>(j, lane) < E) smem[warp * E4 + expert_of<V>(j, lane)] = psum[j];
-        __shared__ int live_of[kWarps];
-        if (lane == 0) live_of[warp] = live_tokens;
+            if (expert_of<L, V>(j, lane) < E) smem[team * E4 + expert_of<L, V>(j, lane)] = psum[j];
+        __shared__ int live_of[kTeams];
+        if (lane == 0) live_of[team] = live_tokens;
         __syncthreads();
         for (int e = threadIdx.x; e < E; e += blockDim.x) {
             float s = 0.0f;
-            for (int w = 0; w < kWarps; ++w) s += smem[w * E4 + e];
+            for (int w = 0; w < kTeams; ++w) s += smem[w * E4 + e];
             p.part_p[static_cast<int64_t>(blockIdx.x) * E + e] = s;
             p.part_count[static_cast<int64_t>(blockIdx.x) * E + e] = count[e];
         }
         if (threadIdx.x == 0) {
             int s = 0;
-            for (int w = 0; w < kWarps; ++w) s += live_of[w];
+            for (int w = 0; w < kTeams; ++w) s += live_of[w];
             p.part_live[blockIdx.x] = s;
         }
     }
@@ -405,13 +420,14 @@ struct RouteGradParams {
 // picked logits alone: a pick's logit gets w (dw - <w, dw>).  Otherwise a
 // weight is its p, and dw joins g.
 // The picks' parts go through a row of shared memory that is zero between tokens.
-template <int VPT, int V>
-__global__ void __launch_bounds__(32 * kWarps, VPT <= 8 ? 4 : 1) route_grad_kernel(RouteGradParams p) {
-    extern __shared__ float smem[];      // [kWarps][experts]
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+template <int L, int VPT, int V>
+__global__ void __launch_bounds__(32 * kWarps, grad_on_sm(VPT)) route_grad_kernel(RouteGradParams p) {
+    constexpr int kTeams = kWarps * 32 / L;
+    extern __shared__ float smem[];      // [kTeams][experts]
+    const int lane = threadIdx.x % L, team = threadIdx.x / L;
     const int E = p.experts, K = p.topk;
-    float *picks = smem + warp * E;
-    for (int e = lane; e < E; e += 32) picks[e] = 0.0f;
+    float *picks = smem + team * E;
+    for (int e = lane; e < E; e += L) picks[e] = 0.0f;
     __syncwarp();
     const float dloss = p.dloss ? *p.dloss : 0.0f;
     constexpr bool kHeld = VPT <= 16;    // the slope stays in registers
@@ -419,10 +435,10 @@ __global__ void __launch_bounds__(32 * kWarps, VPT <= 8 ? 4 : 1) route_grad_kern
     if (kHeld) {
 #pragma unroll
         for (int j = 0; j < VPT; ++j)
-            slope[j] = p.dloss && expert_of<V>(j, lane) < E ? dloss * p.slope[expert_of<V>(j, lane)] : 0.0f;
+            slope[j] = p.dloss && expert_of<L, V>(j, lane) < E ? dloss * p.slope[expert_of<L, V>(j, lane)] : 0.0f;
     }
-    const uint32_t T = static_cast<uint32_t>(p.tokens), stride = gridDim.x * kWarps;
-    uint32_t t = blockIdx.x * kWarps + warp;
+    const uint32_t T = static_cast<uint32_t>(p.tokens), stride = gridDim.x * kTeams;
+    uint32_t t = blockIdx.x * kTeams + team;
     // A token's inputs are on their way while the last one's are worked on.
     // lse is +inf for a padded token and -inf where no logit was left: both
     // have p = 0, whatever the logits hold.
@@ -430,7 +446,7 @@ __global__ void __launch_bounds__(32 * kWarps, VPT <= 8 ? 4 : 1) route_grad_kern
     int idx_ahead = -1;
     auto fetch = [&](uint32_t at) {
         lse_ahead = p.lse[at];
-        load_row<VPT, V>(p.logits, p.bf16, at * p.logits_stride, E, lane, ahead);
+        load_row<L, VPT, V>(p.logits, p.bf16, at * p.logits_stride, E, lane, ahead);
         const uint64_t pick = static_cast<uint64_t>(at) * static_cast<uint32_t>(K) + lane;
         if (lane < K) {
             idx_ahead = p.topk_idx[pick];
@@ -439,32 +455,33 @@ __global__ void __launch_bounds__(32 * kWarps, VPT <= 8 ? 4 : 1) route_grad_kern
         }
     };
     if (t < T) fetch(t);
-    for (; t < T; t += stride) {
+    for (; t - (L == 32 ? 0 : team & 1) < T; t += stride) {
+        const bool inside = t < T;
         const float lse = lse_ahead;
-        const bool live = !isinf(lse);
+        const bool live = inside && !isinf(lse);
         float l[VPT];
 #pragma unroll
         for (int j = 0; j < VPT; ++j) l[j] = ahead[j];
-        const int idx = idx_ahead;
+        const int idx = inside ? idx_ahead : -1;
         float w = idx >= 0 ? w_ahead : 0.0f, add = idx >= 0 ? add_ahead : 0.0f;
         if (t + stride < T) fetch(t + stride);
-        if (p.renormalize) add = w * (add - warp_sum(w * add));
+        if (p.renormalize) add = w * (add - lanes_sum<L>(w * add));
         if (idx >= 0 && idx < E) picks[idx] = add;
         __syncwarp();
         float g[VPT], inner = 0.0f;
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
-            const int e = expert_of<V>(j, lane);
+            const int e = expert_of<L, V>(j, lane);
             l[j] = live ? __expf(l[j] - lse) : 0.0f;
             g[j] = kHeld ? slope[j] : p.dloss && e < E ? dloss * p.slope[e] : 0.0f;
             if (!p.renormalize && e < E) g[j] += picks[e];
             inner = fmaf(l[j], g[j], inner);
         }
-        inner = warp_sum(inner);
+        inner = lanes_sum<L>(inner);
 #pragma unroll
         for (int j = 0; j < VPT; j += V) {
-            const int e = expert_of<V>(j, lane);
-            if (e < E) {
+            const int e = expert_of<L, V>(j, lane);
+            if (e < E && inside) {
                 float d[V];
 #pragma unroll
                 for (int i = 0; i < V; ++i)
@@ -521,23 +538,33 @@ bool by_vector(const void *p, int64_t stride, int experts, int bf16, int v) {
     return experts % v == 0 && stride % v == 0 && aligned(p, static_cast<uintptr_t>(v * (bf16 ? 2 : 4)));
 }
 
-// Calls f with the number of logits a lane holds and the vector's length, as
-// types; can(V): whether vectors of V are allowed.
-template <int VPT, int V, typename C, typename F>
+// Calls f with the lanes to a token, the logits a lane holds and the vector's
+// length, as types; can(V): whether vectors of V are allowed.  Half a warp to a
+// token halves what does not grow with the experts: 131072 tokens of 256 logits,
+// top 8, took 67 us with a whole warp to each and take 47 (64 logits: 54 and 32);
+// past 8 picks the bound of 16 lanes lets too many through.
+template <int L, int VPT, int V, typename C, typename F>
 void with_vector(C can, F f) {
-    if (can(V)) f(std::integral_constant<int, VPT>(), std::integral_constant<int, V>());
-    else f(std::integral_constant<int, VPT>(), std::integral_constant<int, 1>());
+    constexpr std::integral_constant<int, L> l;
+    constexpr std::integral_constant<int, VPT> vpt;
+    if (can(V)) f(l, vpt, std::integral_constant<int, V>());
+    else f(l, vpt, std::integral_constant<int, 1>());
 }
 template <typename C, typename F>
-void by_width(int experts, C can, F f) {
+void by_width(int experts, int topk, C can, F f) {
+    if (topk <= 8 && experts <= 256) {
+        const int v = (experts + 15) / 16;
+        if (v <= 4) with_vector<16, 4, 4>(can, f);
+        else if (v <= 8) with_vector<16, 8, 4>(can, f);
+        else with_vector<16, 16, 4>(can, f);
+        return;
+    }
     const int v = (experts + 31) / 32;
-    if (v <= 1) f(std::integral_constant<int, 1>(), std::integral_constant<int, 1>());
-    else if (v <= 2) with_vector<2, 2>(can, f);
-    else if (v <= 4) with_vector<4, 4>(can, f);
-    else if (v <= 8) with_vector<8, 4>(can, f);
-    else if (v <= 16) with_vector<16, 4>(can, f);
-    else if (v <= 32) with_vector<32, 4>(can, f);
-    else f(std::integral_constant<int, 128>(), std::integral_constant<int, 1>());
+    if (v <= 2) with_vector<32, 2, 2>(can, f);
+    else if (v <= 8) with_vector<32, 8, 4>(can, f);
+    else if (v <= 16) with_vector<32, 16, 4>(can, f);
+    else if (v <= 32) with_vector<32, 32, 4>(can, f);
+    else with_vector<32, 128, 1>(can, f);
 }
 
 }  // namespace
@@ -589,21 +616,25 @@ ep_status ep_route(int64_t tokens, int32_t experts, int32_t topk, const void *lo
         p.part_live = p.part_count + static_cast<int64_t>(blocks) * experts;
         p.done = reinterpret_cast<unsigned int *>(p.part_live + blocks);
     }
+    int parts = 0;
     if (tokens > 0) {
         const int sms = sm_count_of(c.device);
         if (sms < 1) return EP_ERR_CUDA;
-        const int64_t most = (tokens + kWarps - 1) / kWarps;
-        const int grid = train ? blocks : static_cast<int>(most < 4 * sms ? most : 4 * sms);
-        const size_t smem = sizeof(float) * ((experts + 3) / 4 * 4 * kWarps + (train ? experts : 0));
-        by_width(experts, [&](int v) { return by_vector(logits, logits_stride, experts, p.bf16, v); },
-                 [&](auto vpt, auto v) {
-                     constexpr int VPT = decltype(vpt)::value, V = decltype(v)::value;
+        by_width(experts, topk, [&](int v) { return by_vector(logits, logits_stride, experts, p.bf16, v); },
+                 [&](auto lanes, auto vpt, auto v) {
+                     constexpr int L = decltype(lanes)::value, VPT = decltype(vpt)::value, V = decltype(v)::value;
+                     constexpr int kTeams = kWarps * 32 / L;
+                     const int64_t need = (tokens + kTeams - 1) / kTeams, most = route_on_sm(VPT) * sms;
+                     int grid = static_cast<int>(need < most ? need : most);
+                     if (train && grid > blocks) grid = blocks;
+                     parts = grid;
+                     const size_t smem = sizeof(float) * ((experts + 3) / 4 * 4 * kTeams + (train ? experts : 0));
                      if (train) {
-                         allow_smem(route_kernel<VPT, V, true>, smem);
-                         route_kernel<VPT, V, true><<<grid, 32 * kWarps, smem, st>>>(p);
+                         allow_smem(route_kernel<L, VPT, V, true>, smem);
+                         route_kernel<L, VPT, V, true><<<grid, 32 * kWarps, smem, st>>>(p);
                      } else {
-                         allow_smem(route_kernel<VPT, V, false>, smem);
-                         route_kernel<VPT, V, false><<<grid, 32 * kWarps, smem, st>>>(p);
+                         allow_smem(route_kernel<L, VPT, V, false>, smem);
+                         route_kernel<L, VPT, V, false><<<grid, 32 * kWarps, smem, st>>>(p);
                      }
                  });
     }
@@ -612,7 +643,7 @@ ep_status ep_route(int64_t tokens, int32_t experts, int32_t topk, const void *lo
         BalanceParams b{};
         b.part_p = p.part_p, b.part_count = p.part_count, b.part_live = p.part_live;
         b.done = p.done, b.part_loss = reinterpret_cast<float *>(p.done + 1);
-        b.parts = tokens > 0 ? blocks : 0, b.experts = experts, b.topk = topk, b.coef = coef;
+        b.parts = parts, b.experts = experts, b.topk = topk, b.coef = coef;
         b.expert_count = expert_count, b.loss = loss, b.slope = slope;
         balance_kernel<<<balance_blocks(experts), 1024, 0, st>>>(b);
     }
@@ -643,18 +674,20 @@ ep_status ep_route_backward(int64_t tokens, int32_t experts, int32_t topk, const
     p.experts = experts, p.topk = topk, p.renormalize = renormalize;
     const int sms = sm_count_of(c.device);
     if (sms < 1) return EP_ERR_CUDA;
-    const int64_t blocks = (tokens + kWarps - 1) / kWarps;
-    const unsigned grid = static_cast<unsigned>(blocks < 8 * sms ? blocks : 8 * sms);
-    const size_t smem = sizeof(float) * experts * kWarps;
-    by_width(experts,
+    by_width(experts, topk,
              [&](int v) {
                  return by_vector(logits, logits_stride, experts, p.bf16, v) &&
                         by_vector(dlogits, dlogits_stride, experts, p.bf16, v);
              },
-             [&](auto vpt, auto v) {
-                 auto kernel = route_grad_kernel<decltype(vpt)::value, decltype(v)::value>;
+             [&](auto lanes, auto vpt, auto v) {
+                 constexpr int L = decltype(lanes)::value, VPT = decltype(vpt)::value;
+                 constexpr int kTeams = kWarps * 32 / L;
+                 const int64_t need = (tokens + kTeams - 1) / kTeams, most = 2 * grad_on_sm(VPT) * sms;
+                 auto kernel = route_grad_kernel<L, VPT, decltype(v)::value>;
+                 const size_t smem = sizeof(float) * experts * kTeams;
                  allow_smem(kernel, smem);
-                 kernel<<<grid, 32 * kWarps, smem, static_cast<cudaStream_t>(stream)>>>(p);
+                 kernel<<<static_cast<unsigned>(need < most ? need : most), 32 * kWarps, smem,
+                          static_cast<cudaStream_t>(stream)>>>(p);
              });
     return launched();
 }
