@@ -2,22 +2,23 @@
 // their weights, per-expert counts and the balance loss, and the logits'
 // gradient (include/ep_ops.h).
 //
-// A warp, or half a warp (L lanes: half for up to 256 experts and 8 picks), holds
+// A warp, or half a warp (L lanes: half for up to 256 experts and 12 picks), holds
 // a token's logits in registers, VPT to a lane, in vectors of V neighbouring
 // experts (V = 1 where a row's address or E does not allow more).
 // The K largest are found without sorting:
-//  - the largest logit of each lane is known (of each pair of lanes in a whole
-//    warp with up to 16 picks), and the K-th largest of these, from a bitonic
-//    sort across the lanes, is a bound that at least K logits reach (K
-//    warp-wide maxima in its place cost a third of the kernel);
-//  - the few logits that reach it -- about K + 3 of 256 -- are listed in shared
+//  - the largest logit of each lane is known (for K > 24 the largest two), and
+//    the K-th largest of these, from a bitonic sort across the lanes, is a
+//    bound that at least K logits reach (K warp-wide maxima in its place cost
+//    a third of the kernel; 131072 tokens of 256, top 32: 134 us
+//    against 608 where the list overflows);
+//  - the few logits that reach it -- about 11 of 256 for K = 8 -- are listed in shared
 //    memory as 64-bit words, the logit's bits in the floats' order and then the
 //    expert, so that ties go to the lower one;
 //  - each of them counts the words above its own: that is its place.
 // Bound by issue, not memory; K rounds of a maximum over all logits took 1800
 // instructions a token (131072 tokens of 256 fp32 logits, top 8: 47 us against
-// 207; with the loss and counts 75 us; the gradient, bound by memory more than
-// by issue, 54 us, 5.0 TB/s).
+// 207; with the loss and counts 77 us; the gradient, bound by memory more than
+// by issue, 56 us, 4.8 TB/s).
 #include <type_traits>
 
 #include "ep_ops.cuh"
@@ -73,50 +74,66 @@ __device__ __forceinline__ float lanes_sum(float v) {
     return v;
 }
 
-// Loads a lane's logits; what lies past the experts is -inf.  For V > 1 the
-// experts and the row's address are multiples of V.
+// Loads a lane's logits as they lie in memory; what lies past the experts is
+// -inf.  For V > 1 the experts and the row's address are multiples of V.
+// Nothing here waits for the load: values() makes the numbers, when they are
+// needed.  (Converted at once, 131072 rows of 512
+// bf16 logits, top 8, took 127 us, and take 87; the gradient 178 and 105.)
 template <int L, int VPT, int V>
-__device__ __forceinline__ void load_row(const void *logits, int bf16, int64_t at, int experts, int lane, float (&l)[VPT]) {
+__device__ __forceinline__ void load_row(const void *logits, int bf16, int64_t at, int experts, int lane,
+                                         uint32_t (&raw)[VPT]) {
 #pragma unroll
     for (int j = 0; j < VPT; j += V) {
         const int e = expert_of<L, V>(j, lane);
         if (e >= experts) {
 #pragma unroll
-            for (int i = 0; i < V; ++i) l[j + i] = -INFINITY;
+            for (int i = 0; i < V; ++i) raw[j + i] = bf16 ? 0xff80ff80u : 0xff800000u;
         } else if (bf16) {
-            const __nv_bfloat16 *from = static_cast<const __nv_bfloat16 *>(logits) + at + e;
+            const uint16_t *from = static_cast<const uint16_t *>(logits) + at + e;
             if constexpr (V == 4) {
                 const uint2 u = *reinterpret_cast<const uint2 *>(from);
-                unpack2(u.x, l[j], l[j + 1]);
-                unpack2(u.y, l[j + 2], l[j + 3]);
+                raw[j] = u.x, raw[j + 1] = u.y;
             } else if constexpr (V == 2) {
-                unpack2(*reinterpret_cast<const uint32_t *>(from), l[j], l[j + 1]);
+                raw[j] = *reinterpret_cast<const uint32_t *>(from);
             } else {
-                l[j] = __bfloat162float(*from);
+                raw[j] = *from;
             }
         } else {
-            const float *from = static_cast<const float *>(logits) + at + e;
+            const uint32_t *from = static_cast<const uint32_t *>(logits) + at + e;
             if constexpr (V == 4) {
-                const float4 u = *reinterpret_cast<const float4 *>(from);
-                l[j] = u.x, l[j + 1] = u.y, l[j + 2] = u.z, l[j + 3] = u.w;
+                const uint4 u = *reinterpret_cast<const uint4 *>(from);
+                raw[j] = u.x, raw[j + 1] = u.y, raw[j + 2] = u.z, raw[j + 3] = u.w;
             } else if constexpr (V == 2) {
-                const float2 u = *reinterpret_cast<const float2 *>(from);
-                l[j] = u.x, l[j + 1] = u.y;
+                const uint2 u = *reinterpret_cast<const uint2 *>(from);
+                raw[j] = u.x, raw[j + 1] = u.y;
             } else {
-                l[j] = *from;
+                raw[j] = *from;
             }
         }
     }
 }
+template <int VPT, int V>
+__device__ __forceinline__ void values(const uint32_t (&raw)[VPT], int bf16, float (&l)[VPT]) {
+    if (bf16) {
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {      // V of them in the first V / 2 words (one word for V = 1)
+            const uint32_t u = raw[j / V * V + j % V / 2];
+            l[j] = __uint_as_float(j % V % 2 ? u & 0xffff0000u : u << 16);
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) l[j] = __uint_as_float(raw[j]);
+    }
+}
 
-// Sorts a value of each of L lanes, largest first, by exchanges over distances
-// from kPair up (kPair = 2: lanes of a pair hold the same value).
-template <int L, int kPair>
+// Sorts a value of each of L lanes, largest first, by exchanges; from = L for
+// values that rise and then fall, or fall and then rise, across the lanes.
+template <int L, int from = 2>
 __device__ __forceinline__ float sort_lanes(float v, int lane) {
 #pragma unroll
-    for (int k = 2 * kPair; k <= L; k *= 2)
+    for (int k = from; k <= L; k *= 2)
 #pragma unroll
-        for (int j = k / 2; j >= kPair; j /= 2) {
+        for (int j = k / 2; j > 0; j /= 2) {
             const float o = __shfl_xor_sync(0xffffffffu, v, j);
             const bool larger = ((lane & j) == 0) == ((lane & k) == 0 || k == L);
             v = larger ? fmaxf(v, o) : fminf(v, o);
@@ -137,15 +154,23 @@ __device__ __forceinline__ unsigned long long pick(const float (&l)[VPT], int E,
 #pragma unroll
     for (int j = 1; j < VPT; ++j) most = fmaxf(most, l[j]);      // NaN is passed over
     most = most > -INFINITY ? most : -INFINITY;
-    float bound;
-    if (L == 32 && K <= 16) {
-        most = sort_lanes<L, 2>(fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1)), lane);
-        bound = __shfl_sync(0xffffffffu, most, 2 * (K - 1), L);
-    } else {
-        most = sort_lanes<L, 1>(most, lane);
-        bound = __shfl_sync(0xffffffffu, most, K - 1, L);
-    }
+    most = sort_lanes<L>(most, lane);
     top = __shfl_sync(0xffffffffu, most, 0, L);
+    if (L == 32 && K > 24) {
+        // of the largest two of each lane: as many as the lanes' largest alone
+        // let pass would not fit on the list.  For two lists in order, the
+        // larger of one's i-th and the other's i-th from its end are the
+        // largest 32 of both.
+        float second = -INFINITY, first = -INFINITY;
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            second = fmaxf(second, fminf(first, l[j] > -INFINITY ? l[j] : -INFINITY));
+            first = fmaxf(first, l[j]);
+        }
+        second = sort_lanes<L>(second, lane);
+        most = sort_lanes<L, L>(fmaxf(most, __shfl_sync(0xffffffffu, second, L - 1 - lane)), lane);
+    }
+    const float bound = __shfl_sync(0xffffffffu, most, K - 1, L);
     // fewer than K of them: every logit above -inf is on the list
     const float least = bound > -INFINITY ? bound : -3.402823466e38f;
     // the logits where any lane can read them, and the experts on the list: a
@@ -254,19 +279,15 @@ __global__ void __launch_bounds__(32 * kWarps, route_on_sm(VPT)) route_kernel(Ro
     uint32_t t = blockIdx.x * kTeams + team;
     // A token's logits are on their way while the last one's are worked on, where they fit twice.
     constexpr bool kAhead = VPT <= 16;
-    float ahead[kAhead ? VPT : 1];
+    uint32_t ahead[VPT];
     bool live_ahead = t < T && (p.mask == nullptr || p.mask[t] != 0);
     if constexpr (kAhead) load_row<L, VPT, V>(p.logits, p.bf16, t * p.logits_stride, live_ahead ? E : 0, lane, ahead);
     // both tokens of a warp go on until the first is past the end; a token past it is a padded one that is not stored
     for (; t - (L == 32 ? 0 : team & 1) < T; t += stride) {
         float l[VPT];
         const bool inside = t < T, live = live_ahead;
-        if constexpr (kAhead) {
-#pragma unroll
-            for (int j = 0; j < VPT; ++j) l[j] = ahead[j];
-        } else {
-            load_row<L, VPT, V>(p.logits, p.bf16, t * p.logits_stride, live ? E : 0, lane, l);
-        }
+        if constexpr (!kAhead) load_row<L, VPT, V>(p.logits, p.bf16, t * p.logits_stride, live ? E : 0, lane, ahead);
+        values<VPT, V>(ahead, p.bf16, l);
         live_ahead = t + stride < T && (p.mask == nullptr || p.mask[t + stride] != 0);
         if constexpr (kAhead)
             load_row<L, VPT, V>(p.logits, p.bf16, (t + stride) * p.logits_stride, live_ahead ? E : 0, lane, ahead);
@@ -439,14 +460,19 @@ __global__ void __launch_bounds__(32 * kWarps, grad_on_sm(VPT)) route_grad_kerne
     }
     const uint32_t T = static_cast<uint32_t>(p.tokens), stride = gridDim.x * kTeams;
     uint32_t t = blockIdx.x * kTeams + team;
-    // A token's inputs are on their way while the last one's are worked on.
+    // A token's inputs are on their way while the last one's are worked on, its
+    // logits where they fit twice; wider rows also read their slopes twice
+    // rather than hold them (8192 rows of 4096 bf16 logits: 130 us against 366
+    // for both held, one logit at a time).
+    constexpr bool kTwice = VPT <= 32;
     // lse is +inf for a padded token and -inf where no logit was left: both
     // have p = 0, whatever the logits hold.
-    float ahead[VPT], lse_ahead = 0.0f, w_ahead = 0.0f, add_ahead = 0.0f;
+    uint32_t ahead[VPT];
+    float lse_ahead = 0.0f, w_ahead = 0.0f, add_ahead = 0.0f;
     int idx_ahead = -1;
     auto fetch = [&](uint32_t at) {
         lse_ahead = p.lse[at];
-        load_row<L, VPT, V>(p.logits, p.bf16, at * p.logits_stride, E, lane, ahead);
+        if (kTwice) load_row<L, VPT, V>(p.logits, p.bf16, at * p.logits_stride, E, lane, ahead);
         const uint64_t pick = static_cast<uint64_t>(at) * static_cast<uint32_t>(K) + lane;
         if (lane < K) {
             idx_ahead = p.topk_idx[pick];
@@ -460,22 +486,27 @@ __global__ void __launch_bounds__(32 * kWarps, grad_on_sm(VPT)) route_grad_kerne
         const float lse = lse_ahead;
         const bool live = inside && !isinf(lse);
         float l[VPT];
-#pragma unroll
-        for (int j = 0; j < VPT; ++j) l[j] = ahead[j];
+        if (!kTwice) load_row<L, VPT, V>(p.logits, p.bf16, t * p.logits_stride, E, lane, ahead);
+        values<VPT, V>(ahead, p.bf16, l);
         const int idx = inside ? idx_ahead : -1;
         float w = idx >= 0 ? w_ahead : 0.0f, add = idx >= 0 ? add_ahead : 0.0f;
         if (t + stride < T) fetch(t + stride);
         if (p.renormalize) add = w * (add - lanes_sum<L>(w * add));
         if (idx >= 0 && idx < E) picks[idx] = add;
         __syncwarp();
-        float g[VPT], inner = 0.0f;
+        auto slope_at = [&](int j) {
+            const int e = expert_of<L, V>(j, lane);
+            float g = kHeld ? slope[j] : p.dloss && e < E ? dloss * p.slope[e] : 0.0f;
+            if (!p.renormalize && e < E) g += picks[e];
+            return g;
+        };
+        float g[kTwice ? VPT : 1], inner = 0.0f;
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
-            const int e = expert_of<L, V>(j, lane);
             l[j] = live ? __expf(l[j] - lse) : 0.0f;
-            g[j] = kHeld ? slope[j] : p.dloss && e < E ? dloss * p.slope[e] : 0.0f;
-            if (!p.renormalize && e < E) g[j] += picks[e];
-            inner = fmaf(l[j], g[j], inner);
+            const float v = slope_at(j);
+            if constexpr (kTwice) g[j] = v;
+            inner = fmaf(l[j], v, inner);
         }
         inner = lanes_sum<L>(inner);
 #pragma unroll
@@ -484,8 +515,12 @@ __global__ void __launch_bounds__(32 * kWarps, grad_on_sm(VPT)) route_grad_kerne
             if (e < E && inside) {
                 float d[V];
 #pragma unroll
-                for (int i = 0; i < V; ++i)
-                    d[i] = (live ? l[j + i] * (g[j + i] - inner) : 0.0f) + (p.renormalize ? picks[e + i] : 0.0f);
+                for (int i = 0; i < V; ++i) {
+                    float v;
+                    if constexpr (kTwice) v = g[j + i];
+                    else v = slope_at(j + i);
+                    d[i] = (live ? l[j + i] * (v - inner) : 0.0f) + (p.renormalize ? picks[e + i] : 0.0f);
+                }
                 if (p.bf16) {
                     __nv_bfloat16 *to = static_cast<__nv_bfloat16 *>(p.dlogits) + t * p.dlogits_stride + e;
                     if constexpr (V == 4) *reinterpret_cast<uint2 *>(to) = make_uint2(pack2(d[0], d[1]), pack2(d[2], d[3]));
@@ -542,7 +577,7 @@ bool by_vector(const void *p, int64_t stride, int experts, int bf16, int v) {
 // length, as types; can(V): whether vectors of V are allowed.  Half a warp to a
 // token halves what does not grow with the experts: 131072 tokens of 256 logits,
 // top 8, took 67 us with a whole warp to each and take 47 (64 logits: 54 and 32);
-// past 8 picks the bound of 16 lanes lets too many through.
+// past 12 picks the bound of 16 lanes lets too many through.
 template <int L, int VPT, int V, typename C, typename F>
 void with_vector(C can, F f) {
     constexpr std::integral_constant<int, L> l;
@@ -550,9 +585,12 @@ void with_vector(C can, F f) {
     if (can(V)) f(l, vpt, std::integral_constant<int, V>());
     else f(l, vpt, std::integral_constant<int, 1>());
 }
-template <typename C, typename F>
+// kWideV: the vectors of rows of more than 1024.  The router's sums and logits
+// fill the registers, and vectors of 4 cost more of them than they save: 8192
+// rows of 4096 fp32 logits take 139 us with one at a time, 186 with four.
+template <int kWideV, typename C, typename F>
 void by_width(int experts, int topk, C can, F f) {
-    if (topk <= 8 && experts <= 256) {
+    if (topk <= 12 && experts <= 256) {
         const int v = (experts + 15) / 16;
         if (v <= 4) with_vector<16, 4, 4>(can, f);
         else if (v <= 8) with_vector<16, 8, 4>(can, f);
@@ -564,7 +602,7 @@ void by_width(int experts, int topk, C can, F f) {
     else if (v <= 8) with_vector<32, 8, 4>(can, f);
     else if (v <= 16) with_vector<32, 16, 4>(can, f);
     else if (v <= 32) with_vector<32, 32, 4>(can, f);
-    else with_vector<32, 128, 1>(can, f);
+    else with_vector<32, 128, kWideV>(can, f);
 }
 
 }  // namespace
@@ -620,7 +658,7 @@ ep_status ep_route(int64_t tokens, int32_t experts, int32_t topk, const void *lo
     if (tokens > 0) {
         const int sms = sm_count_of(c.device);
         if (sms < 1) return EP_ERR_CUDA;
-        by_width(experts, topk, [&](int v) { return by_vector(logits, logits_stride, experts, p.bf16, v); },
+        by_width<1>(experts, topk, [&](int v) { return by_vector(logits, logits_stride, experts, p.bf16, v); },
                  [&](auto lanes, auto vpt, auto v) {
                      constexpr int L = decltype(lanes)::value, VPT = decltype(vpt)::value, V = decltype(v)::value;
                      constexpr int kTeams = kWarps * 32 / L;
@@ -674,7 +712,7 @@ ep_status ep_route_backward(int64_t tokens, int32_t experts, int32_t topk, const
     p.experts = experts, p.topk = topk, p.renormalize = renormalize;
     const int sms = sm_count_of(c.device);
     if (sms < 1) return EP_ERR_CUDA;
-    by_width(experts, topk,
+    by_width<4>(experts, topk,
              [&](int v) {
                  return by_vector(logits, logits_stride, experts, p.bf16, v) &&
                         by_vector(dlogits, dlogits_stride, experts, p.bf16, v);
