@@ -750,3 +750,19 @@ def test_pick_sum_with_long_segments(ep):
         want = (w[..., None] * y[at].double()).sum(1)
         near(got, want, want.abs() * HALF_BF + (w[..., None] * y[at].double()).abs().sum(1) * 3 * U)
         layer.close()
+
+
+@pytest.mark.parametrize("E,K", [(E, K) for E in (12, 64, 100, 250, 256, 260, 512, 1000, 1028, 4096)
+                                 for K in (1, 12, 13, 24, 25, 32) if K <= E])
+def test_route_at_the_bounds_of_its_forms(ep, E, K):
+    """Odd tokens hold few values, so that their lists of candidates run over while their neighbours' do not."""
+    g = gen(E * 33 + K)
+    logits = rnd(g, 75, E) * 3
+    logits[1::4] = torch.randint(0, 3, (19, E), device="cuda", generator=g).float()
+    logits[3::8] = 0.5
+    logits[7::8, K // 2:] = R.NEG
+    for x in (logits, logits.to(BF), logits[:2], logits[1:2]):
+        got, want = check_route(ep, x, K, True, None, 0.5)
+        d = ep.route_backward(x, got, torch.ones(x.shape[0], K, device="cuda"))
+        assert torch.isfinite(d).all() and d.shape == x.shape
+        assert torch.equal(ep.route(x, K).topk_idx, got.topk_idx)
