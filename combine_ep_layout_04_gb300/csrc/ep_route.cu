@@ -2,8 +2,8 @@
 // their weights, per-expert counts and the balance loss, and the logits'
 // gradient (include/ep_ops.h).
 //
-// A warp, or half a warp (L lanes: half for up to 256 experts and 12 picks), holds
-// a token's logits in registers, VPT to a lane, in vectors of V neighbouring
+// A warp, half a warp or a quarter of one (L lanes: half for up to 256 experts
+// and 12 picks, a quarter for up to 64 and 6) holds a token's logits in registers, VPT to a lane, in vectors of V neighbouring
 // experts (V = 1 where a row's address or E does not allow more).
 // The K largest are found without sorting:
 //  - the largest logit of each lane is known (for K > 24 the largest two), and
@@ -148,7 +148,8 @@ template <int L, int VPT, int V>
 __device__ __forceinline__ unsigned long long pick(const float (&l)[VPT], int E, int K, int lane, float *row,
                                                    unsigned long long *words, unsigned long long *picks, float &top) {
     constexpr int kWords = 2 * L;
-    const int shift = L == 32 ? 0 : threadIdx.x & 16;      // where the token's lanes are in a ballot
+    const int shift = threadIdx.x & (32 - L);      // where the token's lanes are in a ballot
+    constexpr uint32_t all = 0xffffffffu >> (32 - L);
     const uint32_t below = (1u << lane) - 1u;
     float most = l[0];
 #pragma unroll
@@ -193,7 +194,7 @@ __device__ __forceinline__ unsigned long long pick(const float (&l)[VPT], int E,
 #pragma unroll
         for (int j = j0; j < VPT && j < j0 + 32; ++j) on |= l[j] >= least ? 1u << (j - j0) : 0u;
         for (uint32_t any = __ballot_sync(0xffffffffu, on != 0); any; any = __ballot_sync(0xffffffffu, on != 0)) {
-            const uint32_t lanes = L == 32 ? any : any >> shift & 0xffffu;
+            const uint32_t lanes = any >> shift & all;
             const int j = j0 + __ffs(on) - 1, at = n + __popc(lanes & below);
             if (on && at < kWords) experts[at] = expert_of<L, V>(j, lane);
             on &= on - 1;
@@ -209,8 +210,9 @@ __device__ __forceinline__ unsigned long long pick(const float (&l)[VPT], int E,
     words[lane] = a;                     // the list ends in zeros
     words[lane + L] = b;
     __syncwarp();
-    // the longer list of the two tokens of a warp
-    const int longest = L == 32 ? listed : max(listed, __shfl_xor_sync(0xffffffffu, listed, 16));
+    int longest = listed;                // of the warp's tokens
+#pragma unroll
+    for (int o = L; o < 32; o *= 2) longest = max(longest, __shfl_xor_sync(0xffffffffu, longest, o));
     int above_a = 0, above_b = 0;
     for (int q = 0; q < longest; q += 4) {
         const ulonglong2 u = *reinterpret_cast<const ulonglong2 *>(words + q);
@@ -282,8 +284,8 @@ __global__ void __launch_bounds__(32 * kWarps, route_on_sm(VPT)) route_kernel(Ro
     uint32_t ahead[VPT];
     bool live_ahead = t < T && (p.mask == nullptr || p.mask[t] != 0);
     if constexpr (kAhead) load_row<L, VPT, V>(p.logits, p.bf16, t * p.logits_stride, live_ahead ? E : 0, lane, ahead);
-    // both tokens of a warp go on until the first is past the end; a token past it is a padded one that is not stored
-    for (; t - (L == 32 ? 0 : team & 1) < T; t += stride) {
+    // the tokens of a warp go on until the first is past the end; one past it is a padded one that is not stored
+    for (; t - team % (32 / L) < T; t += stride) {
         float l[VPT];
         const bool inside = t < T, live = live_ahead;
         if constexpr (!kAhead) load_row<L, VPT, V>(p.logits, p.bf16, t * p.logits_stride, live ? E : 0, lane, ahead);
@@ -481,7 +483,7 @@ __global__ void __launch_bounds__(32 * kWarps, grad_on_sm(VPT)) route_grad_kerne
         }
     };
     if (t < T) fetch(t);
-    for (; t - (L == 32 ? 0 : team & 1) < T; t += stride) {
+    for (; t - team % (32 / L) < T; t += stride) {
         const bool inside = t < T;
         const float lse = lse_ahead;
         const bool live = inside && !isinf(lse);
@@ -574,10 +576,13 @@ bool by_vector(const void *p, int64_t stride, int experts, int bf16, int v) {
 }
 
 // Calls f with the lanes to a token, the logits a lane holds and the vector's
-// length, as types; can(V): whether vectors of V are allowed.  Half a warp to a
-// token halves what does not grow with the experts: 131072 tokens of 256 logits,
-// top 8, took 67 us with a whole warp to each and take 47 (64 logits: 54 and 32);
-// past 12 picks the bound of 16 lanes lets too many through.
+// length, as types; can(V): whether vectors of V are allowed.  Less of a warp to
+// a token means fewer instructions that do not grow with the experts: 131072
+// tokens of 256 logits, top 8, took 67 us with a whole warp to each and take 47
+// with half of one; of 64 logits, top 6, 54, 32 and, with a quarter, 26.  With
+// many picks the bound of few lanes lets too many through for the list: half a
+// warp takes 71 us for 12 of 256 and 263 for 16 (a whole one 74 and 82), a
+// quarter 26 for 6 of 64 and 57 for 8 (half 32 and 35).
 template <int L, int VPT, int V, typename C, typename F>
 void with_vector(C can, F f) {
     constexpr std::integral_constant<int, L> l;
@@ -590,6 +595,10 @@ void with_vector(C can, F f) {
 // rows of 4096 fp32 logits take 139 us with one at a time, 186 with four.
 template <int kWideV, typename C, typename F>
 void by_width(int experts, int topk, C can, F f) {
+    if (topk <= 6 && experts <= 64) {
+        with_vector<8, 8, 4>(can, f);
+        return;
+    }
     if (topk <= 12 && experts <= 256) {
         const int v = (experts + 15) / 16;
         if (v <= 4) with_vector<16, 4, 4>(can, f);

@@ -752,8 +752,8 @@ def test_pick_sum_with_long_segments(ep):
         layer.close()
 
 
-@pytest.mark.parametrize("E,K", [(E, K) for E in (12, 64, 100, 250, 256, 260, 512, 1000, 1028, 4096)
-                                 for K in (1, 12, 13, 24, 25, 32) if K <= E])
+@pytest.mark.parametrize("E,K", [(E, K) for E in (12, 60, 64, 68, 100, 250, 256, 260, 512, 1000, 1028, 4096)
+                                 for K in (1, 6, 7, 12, 13, 24, 25, 32) if K <= E])
 def test_route_at_the_bounds_of_its_forms(ep, E, K):
     """Odd tokens hold few values, so that their lists of candidates run over while their neighbours' do not."""
     g = gen(E * 33 + K)
